@@ -65,11 +65,13 @@ def draw(rng):
     c = dict(op=op, Hq=Hkv * G, Hkv=Hkv, d=rng.choice([64, 128]), bs=rng.choice([64, 128]), mix=rng.randrange(1 << 30))
     if op == "append":
         B = _log(rng, 1, 32)
-        c.update(B=B, paged=rng.random() < 0.6, new_lo=1, new_hi=_log(rng, 1, 32768 // B), old_lo=0,
+        hi = _log(rng, 1, 32768 // B)
+        c.update(B=B, paged=rng.random() < 0.6, new_lo=rng.choice([1, _up(hi, 2), hi]), new_hi=hi, old_lo=0,
                  old_hi=_log(rng, 1, 4096))
     elif op == "prompt":
         B = _log(rng, 1, 24)
-        c.update(B=B, paged=rng.random() < 0.6, new_lo=1, new_hi=_log(rng, 1, (16384 if Hkv * G <= 32 else 8192) // B), old_lo=0,
+        hi = _log(rng, 1, (16384 if Hkv * G <= 32 else 8192) // B)
+        c.update(B=B, paged=rng.random() < 0.6, new_lo=rng.choice([1, _up(hi, 2), hi]), new_hi=hi, old_lo=0,
                  old_hi=_log(rng, 1, 16384 if B < 4 else 4096))
     elif op == "shared":
         groups = rng.randint(1, 4)
