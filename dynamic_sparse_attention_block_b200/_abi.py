@@ -48,12 +48,19 @@ class PrrStepEvents(ctypes.Structure):
     _fields_ = [(n, _c_void_p) for n in STEP_EVENTS + TIMING_MARKS]
 
 
+class PrrCacheBuffers(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in (
+        "k_cache", "v_cache", "block_table", "page_refs", "seq_lens", "summ", "ema", "pred", "rep_offsets")]
+
+
 # exported C symbols, in header order
 SYMBOLS = (
     "prr_version", "prr_status_string", "prr_workspace_bytes", "prr_workspace_init",
     "prr_get_device_status", "prr_append_kv", "prr_update_summaries", "prr_select_topk",
     "prr_ema_predict", "prr_speculate", "prr_repair_merge", "prr_decode_step",
     "prr_decode_step_fused", "prr_budget_fit", "prr_budget_choose", "prr_select_topk_static",
+    "prr_serving_workspace_bytes", "prr_append_prompt", "prr_attend_prompt", "prr_attend_shared",
+    "prr_cache_reserve", "prr_cache_fork", "prr_cache_release", "prr_cache_compact",
 )
 
 # mirrors PRR_WS_TEST_SKIP_SELECTION_OFFSET in include/prr.h
@@ -66,7 +73,7 @@ SELECT_STATIC_SCRATCH_BYTES = 256 + 65536 * 4 + SELECT_STATIC_MAX_BLOCKS * 4
 STATUS = {0: "PRR_OK", 1: "PRR_ERR_INVALID_ARG", 2: "PRR_ERR_SHAPE", 3: "PRR_ERR_CAPACITY",
           4: "PRR_ERR_CUDA", 5: "PRR_ERR_DEVICE_STATUS", 6: "PRR_ERR_TIMEOUT"}
 DEVICE_STATUS = {0: "ok", 1: "bad seq_len", 2: "bad predicted list", 3: "bad missed list",
-                 4: "wait timed out", 5: "bad summary range"}
+                 4: "wait timed out", 5: "bad summary range", 6: "too few free pages"}
 
 
 class PrrError(RuntimeError):
@@ -112,8 +119,19 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     L.prr_select_topk_static.argtypes = [dims, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.prr_budget_fit.argtypes = [vp, vp, _i32, _i32, vp]
     L.prr_budget_choose.argtypes = [vp, vp, vp, _i32, _i32, _i32, ctypes.POINTER(_i32)]
+    i64 = ctypes.c_int64
+    cache = ctypes.POINTER(PrrCacheBuffers)
+    L.prr_serving_workspace_bytes.restype = sz
+    L.prr_serving_workspace_bytes.argtypes = [dims, _i32]
+    L.prr_append_prompt.argtypes = [dims, vp, vp, i64, vp, _i32, vp, vp, vp, vp, vp, sz, vp]
+    L.prr_attend_prompt.argtypes = [dims, vp, i64, vp, _i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.prr_attend_shared.argtypes = [dims, vp, i64, vp, _i32, vp, vp, _i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.prr_cache_reserve.argtypes = [dims, vp, cache, vp, sz, vp]
+    L.prr_cache_fork.argtypes = [dims, vp, vp, _i32, cache, vp, sz, vp]
+    L.prr_cache_release.argtypes = [dims, vp, _i32, cache, vp, sz, vp]
+    L.prr_cache_compact.argtypes = [dims, cache, vp, vp, vp, sz, vp]
     for name in SYMBOLS:
-        if name not in ("prr_version", "prr_status_string", "prr_workspace_bytes"):
+        if name not in ("prr_version", "prr_status_string", "prr_workspace_bytes", "prr_serving_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
     if path is None:
         _LIB = L
@@ -318,3 +336,121 @@ def prr_decode_step_fused(dims, buffers: PrrStepBuffers, ws, step_parity: int, s
                                         ws.numel() * ws.element_size(), int(step_parity),
                                         _stream(stream)),
            "prr_decode_step_fused")
+
+
+# ----------------------------------------------------------------------------- around the decode step
+# Prompts and page tables.  Calls without a stream run on the current stream of the
+# workspace's device, and every call runs with that device current.
+
+def _rows(t, heads: int, d: int, name: str):
+    """(address, elements between two rows) of packed rows [rows][heads][d] bf16."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16 [rows][{heads}][{d}]")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    rows, (stride, s1, s2) = t.shape[0], t.stride()
+    if rows and (s2 != 1 or (heads > 1 and s1 != d) or (rows > 1 and stride < heads * d)):
+        raise ValueError(f"the heads of one row of {name} must be contiguous, and its rows must not overlap")
+    return t.data_ptr(), stride if rows > 1 else heads * d
+
+
+def _vec(t, n: int, name: str, dtype=torch.int32):
+    """Address of a contiguous device vector of at least n entries."""
+    if t.dtype != dtype or t.numel() < n:
+        raise ValueError(f"{name} must be {dtype} with {n} entries")
+    return _ptr(t)
+
+
+def _serve(fn: str, ws, stream, *args) -> None:
+    """Call fn(*args, ws, ws_bytes, stream) with the workspace's device current; every tensor of the call is on it."""
+    index = ws.device.index
+    call = getattr(load(), fn)
+    if index == torch.cuda.current_device():
+        _check(call(*args, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), fn)
+    else:
+        with torch.cuda.device(index):
+            _check(call(*args, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), fn)
+
+
+def _same_device(ws, *tensors) -> None:
+    if any(t is not None and t.device != ws.device for t in tensors):
+        raise ValueError("every tensor of a call must be on the workspace's device")
+
+
+def _out_rows(out, lse, rows: int, c: PrrDims) -> None:
+    if out.dtype != torch.bfloat16 or tuple(out.shape) != (rows, c.Hq, c.d):
+        raise ValueError(f"out must be bf16 [{rows}][{c.Hq}][{c.d}]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (rows, c.Hq)):
+        raise ValueError(f"lse must be fp32 [{rows}][{c.Hq}]")
+
+
+def prr_serving_workspace_bytes(dims, max_rows: int) -> int:
+    return int(load().prr_serving_workspace_bytes(ctypes.byref(_dims(dims)), int(max_rows)))
+
+
+def cache_buffers(k_cache=None, v_cache=None, block_table=None, page_refs=None, seq_lens=None, summ=None, ema=None,
+                  pred=None, rep_offsets=None) -> PrrCacheBuffers:
+    """The buffers of the prr_cache_* calls (device tensors; None for those that are not kept)."""
+    return PrrCacheBuffers(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(page_refs), _ptr(seq_lens), _ptr(summ),
+                           _ptr(ema), _ptr(pred), _ptr(rep_offsets))
+
+
+def prr_append_prompt(dims, k_rows, v_rows, q_begin, seq_lens, k_cache, v_cache, summ, ws, stream=None) -> None:
+    c = _dims(dims)
+    kp, ks = _rows(k_rows, c.Hkv, c.d, "k_rows")
+    vp, vs = _rows(v_rows, c.Hkv, c.d, "v_rows")
+    if k_rows.shape[0] != v_rows.shape[0] or ks != vs:
+        raise ValueError("k_rows and v_rows must have one shape and one row stride")
+    _same_device(ws, k_rows, v_rows, q_begin, seq_lens, k_cache, v_cache, summ)
+    _serve("prr_append_prompt", ws, stream, ctypes.byref(c), kp, vp, ks, _vec(q_begin, c.B + 1, "q_begin"),
+           k_rows.shape[0], _vec(seq_lens, c.B, "seq_lens"), _ptr(k_cache), _ptr(v_cache), _ptr(summ))
+
+
+def prr_attend_prompt(dims, q, q_begin, seq_lens, k_cache, v_cache, out, lse, ws, stream=None) -> None:
+    c = _dims(dims)
+    qp, qs = _rows(q, c.Hq, c.d, "q")
+    _out_rows(out, lse, q.shape[0], c)
+    _same_device(ws, q, q_begin, seq_lens, k_cache, v_cache, out, lse)
+    _serve("prr_attend_prompt", ws, stream, ctypes.byref(c), qp, qs, _vec(q_begin, c.B + 1, "q_begin"), q.shape[0],
+           _vec(seq_lens, c.B, "seq_lens"), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse))
+
+
+def prr_attend_shared(dims, q, members, group_begin, shared_blocks, seq_lens, k_cache, v_cache, out, lse, ws,
+                      stream=None) -> None:
+    c = _dims(dims)
+    qp, qs = _rows(q, c.Hq, c.d, "q")
+    if q.shape[0] != c.B:
+        raise ValueError(f"q must hold one row for each of the {c.B} sequences")
+    _out_rows(out, lse, c.B, c)
+    _same_device(ws, q, members, group_begin, shared_blocks, seq_lens, k_cache, v_cache, out, lse)
+    groups = shared_blocks.numel()
+    _serve("prr_attend_shared", ws, stream, ctypes.byref(c), qp, qs, _vec(members, 0, "members"), members.numel(),
+           _vec(group_begin, groups + 1, "group_begin"), _vec(shared_blocks, 0, "shared_blocks"), groups,
+           _vec(seq_lens, c.B, "seq_lens"), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse))
+
+
+def prr_cache_reserve(dims, want_lens, cache: PrrCacheBuffers, ws, stream=None) -> None:
+    c = _dims(dims)
+    _same_device(ws, want_lens)
+    _serve("prr_cache_reserve", ws, stream, ctypes.byref(c), _vec(want_lens, c.B, "want_lens"), ctypes.byref(cache))
+
+
+def prr_cache_fork(dims, parents, children, cache: PrrCacheBuffers, ws, stream=None) -> None:
+    c = _dims(dims)
+    _same_device(ws, parents, children)
+    n = children.numel()
+    _serve("prr_cache_fork", ws, stream, ctypes.byref(c), _vec(parents, n, "parents"), _vec(children, n, "children"), n,
+           ctypes.byref(cache))
+
+
+def prr_cache_release(dims, seqs, cache: PrrCacheBuffers, ws, stream=None) -> None:
+    c = _dims(dims)
+    _same_device(ws, seqs)
+    _serve("prr_cache_release", ws, stream, ctypes.byref(c), _vec(seqs, 0, "seqs"), seqs.numel(), ctypes.byref(cache))
+
+
+def prr_cache_compact(dims, cache: PrrCacheBuffers, remap, n_live, ws, stream=None) -> None:
+    c = _dims(dims)
+    _same_device(ws, remap, n_live)
+    _serve("prr_cache_compact", ws, stream, ctypes.byref(c), ctypes.byref(cache), _vec(remap, c.pages, "remap"),
+           _vec(n_live, 1, "n_live"))

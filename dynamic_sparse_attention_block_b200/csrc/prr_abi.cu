@@ -11,7 +11,7 @@
 #include <utility>
 
 #include "prr.h"
-#include "prr_kernels.cuh"
+#include "prr_host.cuh"
 
 using namespace prr;
 
@@ -29,7 +29,9 @@ bool ema_fits(const prr_dims* d) { return prr::ema_smem_bytes(maxnb_of(d)) <= kM
 
 constexpr int kVersion = 100;  // 0.1.0
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+}  // namespace
+
+namespace prr {
 
 bool dims_ok(const prr_dims* d) {
   if (!d) return false;
@@ -51,6 +53,10 @@ bool dims_ok(const prr_dims* d) {
   if (units > 65535) return false;  // grid.y
   return true;
 }
+
+}  // namespace prr
+
+namespace {
 
 // Selection units and the query heads each one scores with.
 struct SelShape {
@@ -90,10 +96,9 @@ WsLayout layout_for(const prr_dims* d) {
   return L;
 }
 
-struct DeviceInfo {
-  int sms = 0;
-  int prio_high = 0, prio_low = 0;
-};
+}  // namespace
+
+namespace prr {
 
 DeviceInfo device_info() {
   static std::mutex mu;
@@ -114,6 +119,10 @@ DeviceInfo device_info() {
   return cache[dev];
 }
 
+}  // namespace prr
+
+namespace {
+
 // Blocks per selection CTA: about one CTA per SM over the whole (units x blocks) scan,
 // a multiple of 128 so every warp of the CTA streams at least one 32-block tile.
 int select_chunk(int units, int maxnb, int sms) {
@@ -125,9 +134,13 @@ int select_chunk(int units, int maxnb, int sms) {
   return static_cast<int>(c);
 }
 
+}  // namespace
+
+namespace prr {
+
 // Kernel parameters.  `kv_units`: the call works on KV heads whatever the selector
 // (summaries, appends); otherwise units follow the selector.
-Params base_params(const prr_dims* d, void* ws, bool kv_units = false) {
+Params base_params(const prr_dims* d, void* ws, bool kv_units) {
   Params p;
   std::memset(&p, 0, sizeof p);
   p.B = d->B;
@@ -177,6 +190,10 @@ Params base_params(const prr_dims* d, void* ws, bool kv_units = false) {
   return p;
 }
 
+}  // namespace prr
+
+namespace {
+
 // Record a timing mark; under stream capture it must become a real event-record node.
 cudaError_t record_mark(cudaEvent_t ev, cudaStream_t s) {
   if (!ev) return cudaSuccess;
@@ -201,6 +218,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+namespace prr {
+
 // 3-D map over a KV cache, box {64 channels, bs tokens, 1 slice}, 128-byte swizzle, zero
 // fill outside the tensor.  Contiguous caches [B*Hkv][cap][d]: a slice is one
 // (sequence, KV head) pair.  Paged pools [pages*Hkv][bs][d]: a slice is one (page, KV
@@ -220,14 +241,6 @@ bool make_kv_map(CUtensorMap* map, const void* base, const prr_dims* d) {
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-prr_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PRR_OK : PRR_ERR_CUDA; }
-
-}  // namespace
-
-namespace prr {
 
 cudaError_t allow_max_smem(const void* kernel) {
   static std::mutex mu;

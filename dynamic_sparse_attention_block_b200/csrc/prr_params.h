@@ -15,6 +15,7 @@ enum : int {
   kDevBadMissed = 3,       // missed list entry out of range
   kDevWaitTimeout = 4,     // a bounded mbarrier wait gave up
   kDevBadRange = 5,        // summary update range outside [0, cap_tokens]
+  kDevNoPages = 6,         // too few free pages
 };
 
 // Counters of prr_step_buffers::stats.

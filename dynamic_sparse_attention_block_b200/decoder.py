@@ -6,6 +6,7 @@ libprr_b200.so through the C ABI.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional
 
@@ -27,10 +28,12 @@ class PRRDecoder:
     """
 
     def __init__(self, dims: Dims, device: Optional[torch.device] = None,
-                 block_table: Optional[torch.Tensor] = None, rep_offsets: Optional[torch.Tensor] = None):
+                 block_table: Optional[torch.Tensor] = None, rep_offsets: Optional[torch.Tensor] = None,
+                 empty: bool = False):
         """dims.pages > 0 makes the KV cache a paged pool [pages][Hkv][bs][d];
         `block_table` (int32 [B][maxnb], page of block j of sequence b) then defaults to
-        block j of sequence b in page b*maxnb + j.  The representative-key selector
+        block j of sequence b in page b*maxnb + j; with `empty` no sequence holds a page,
+        and reserve() hands them out.  The representative-key selector
         takes `rep_offsets` (uint8 [B][Hkv][maxnb][n_rep], offsets of each block's
         representative tokens inside the block)."""
         if not torch.cuda.is_available():
@@ -42,11 +45,17 @@ class PRRDecoder:
         S = dims.sel_heads  # selections per sequence (per-unit arrays are [B][S][...])
         maxnb = dims.maxnb
         self.block_table = None
+        self.page_refs = None
+        if empty and (dims.pages == 0 or block_table is not None):
+            raise ValueError("empty starts a paged cache without a block table")
         if dims.pages > 0:
-            if block_table is None:
+            if empty:
+                block_table = torch.full((B, maxnb), -1, dtype=torch.int32)
+            elif block_table is None:
                 block_table = torch.arange(B * maxnb, dtype=torch.int32).view(B, maxnb)
             self.block_table = block_table.to(device=dev, dtype=torch.int32).contiguous()
             self.table_host = self.block_table.cpu().numpy()
+            self.page_refs = self._count_refs(dims.pages).to(dev)
             dims = dataclasses.replace(dims, block_table=self.block_table.data_ptr())
             self.k_cache = torch.zeros((dims.pages, Hkv, dims.bs, d), dtype=torch.bfloat16, device=dev)
         else:
@@ -95,6 +104,14 @@ class PRRDecoder:
         self.fused_parity = 0  # control-word copy of the next fused launch
         self.trace = None      # optional per-item timeline of fused launches (enable_trace)
         self.stats = None      # optional step counters (enable_stats)
+        self.serve_ws = None   # workspace of the calls around the step (_serving)
+        if empty and P > 0:    # what the zero state predicts
+            self.pred_buf.copy_(torch.arange(P, dtype=torch.int32, device=dev))
+
+    def _count_refs(self, pages: int) -> torch.Tensor:
+        """How many table entries hold each page (int32 [pages], on the host)."""
+        held = self.table_host[(self.table_host >= 0) & (self.table_host < pages)]
+        return torch.from_numpy(held.reshape(-1)).long().bincount(minlength=pages).to(torch.int32)
 
     # ------------------------------------------------------------------ views
     @property
@@ -245,6 +262,7 @@ class PRRDecoder:
             if self.block_table is not None:
                 self.block_table.copy_(ck["block_table"])
                 self.table_host = ck["block_table"].numpy().copy()
+                self.page_refs.copy_(self._count_refs(self.dims.pages))
             self.parity, self.fused_parity = 0, 0
             self.pred_buf[0].copy_(ck["pred"])
             _abi.prr_workspace_init(self.ws, self.select_stream)
@@ -300,8 +318,106 @@ class PRRDecoder:
         if swap and self.dims.P > 0:
             self.parity ^= 1
 
+    # ------------------------------------------------------------------ around the step
+    # Prompts and pages.  These run on the step stream, after the caller's current stream;
+    # the caller's stream then waits for them, so their results can be used on it at once.
+
+    @contextlib.contextmanager
+    def _serving(self, rows: int = 1):
+        """The serving workspace, large enough for `rows` packed rows (allocated when a
+        call first needs it, or more of it), with the step stream current."""
+        cur = torch.cuda.current_stream(self.device)
+        self._after_caller(self.select_stream)
+        with torch.cuda.stream(self.select_stream):
+            need = _abi.prr_serving_workspace_bytes(self.dims, max(rows, 1))
+            if need == 0:
+                raise ValueError(f"unsupported number of rows {rows}")
+            if self.serve_ws is None or self.serve_ws.numel() < need:
+                status = 0 if self.serve_ws is None else self.serve_ws[:4].clone()
+                self.serve_ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
+                self.serve_ws[:4] = status
+            yield self.serve_ws
+        if cur != self.select_stream:
+            cur.wait_stream(self.select_stream)
+
+    def _ints(self, x) -> torch.Tensor:
+        return torch.as_tensor(x, dtype=torch.int32).to(self.device).contiguous()
+
+    def cache_buffers(self) -> _abi.PrrCacheBuffers:
+        """The paged cache and the state that goes with its sequences (prr_cache_* calls)."""
+        if self.page_refs is None:
+            raise ValueError("pages are shared, reserved and moved in a paged cache only (dims.pages > 0)")
+        return _abi.cache_buffers(self.k_cache, self.v_cache, self.block_table, self.page_refs, self.seq_lens, self.summ,
+                                  self.ema, self.pred if self.dims.P > 0 else None, self.rep_offsets)
+
+    def reserve(self, want_lens) -> None:
+        """Give every sequence b pages for want_lens[b] tokens (int32 [B]); it keeps those it holds."""
+        with self._serving() as ws:
+            _abi.prr_cache_reserve(self.dims, self._ints(want_lens), self.cache_buffers(), ws)
+
+    def fork(self, parents, children) -> None:
+        """Make the empty sequences children[i] copies of parents[i]: shared pages, a copy
+        of the partly filled last one, and the summaries, EMA state and prediction."""
+        with self._serving() as ws:
+            _abi.prr_cache_fork(self.dims, self._ints(parents), self._ints(children), self.cache_buffers(), ws)
+
+    def release(self, seqs) -> None:
+        """Give back the pages of the sequences; their slots are empty afterwards."""
+        with self._serving() as ws:
+            _abi.prr_cache_release(self.dims, self._ints(seqs), self.cache_buffers(), ws)
+
+    def compact(self):
+        """Move the live pages to the front of the pool.  Returns (remap [pages], n_live [1]) on the device."""
+        with self._serving() as ws:
+            remap = torch.empty((self.dims.pages,), dtype=torch.int32, device=self.device)
+            n_live = torch.empty((1,), dtype=torch.int32, device=self.device)
+            _abi.prr_cache_compact(self.dims, self.cache_buffers(), remap, n_live, ws)
+        return self._lent(remap), self._lent(n_live)
+
+    def _lent(self, t: torch.Tensor) -> torch.Tensor:
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
+    def append_prompt(self, k_rows: torch.Tensor, v_rows: torch.Tensor, q_begin) -> None:
+        """Append packed rows k_rows / v_rows [rows][Hkv][d] bf16 behind the sequences'
+        tokens (sequence b: rows q_begin[b] .. q_begin[b+1]), with their block summaries."""
+        with self._serving(k_rows.shape[0]) as ws:
+            _abi.prr_append_prompt(self.dims, k_rows, v_rows, self._ints(q_begin), self.seq_lens, self.k_cache,
+                                   self.v_cache, self.summ, ws)
+
+    def attend_prompt(self, q: torch.Tensor, q_begin, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None):
+        """Causal attention of packed rows q [rows][Hq][d] bf16, the newest rows of their
+        sequences (appended before).  Returns (out [rows][Hq][d] bf16, lse [rows][Hq] fp32)."""
+        with self._serving(q.shape[0]) as ws:
+            out, lse = self._attend_outputs(q, out, lse)
+            _abi.prr_attend_prompt(self.dims, q, self._ints(q_begin), self.seq_lens, self.k_cache, self.v_cache, out, lse, ws)
+        return self._lent(out), self._lent(lse)
+
+    def attend_shared(self, q: torch.Tensor, members, group_begin, shared_blocks, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None):
+        """Attention of q [B][Hq][d] bf16 over all tokens of each sequence, in groups whose
+        first shared_blocks[g] blocks are the same and read once.  Returns (out, lse)."""
+        with self._serving() as ws:
+            out, lse = self._attend_outputs(q, out, lse)
+            _abi.prr_attend_shared(self.dims, q, self._ints(members), self._ints(group_begin), self._ints(shared_blocks),
+                                   self.seq_lens, self.k_cache, self.v_cache, out, lse, ws)
+        return self._lent(out), self._lent(lse)
+
+    def _attend_outputs(self, q, out, lse):
+        d = self.dims
+        if out is None:
+            out = torch.zeros((q.shape[0], d.Hq, d.d), dtype=torch.bfloat16, device=self.device)
+        if lse is None:
+            lse = torch.zeros((q.shape[0], d.Hq), dtype=torch.float32, device=self.device)
+        return out, lse
+
     def device_status(self) -> int:
-        return _abi.prr_get_device_status(self.ws)
+        """Device status code of the steps, or if that is 0 of the calls around them."""
+        code = _abi.prr_get_device_status(self.ws)
+        if code == 0 and self.serve_ws is not None:
+            code = _abi.prr_get_device_status(self.serve_ws)
+        return code
 
 
 KINDS = {1: "sel", 2: "spec", 3: "repair", 4: "ema", 5: "combine", 6: "finish"}

@@ -94,6 +94,7 @@ typedef enum {
 #define PRR_DEV_BAD_MISSED 3   /* missed list entry out of range */
 #define PRR_DEV_WAIT_TIMEOUT 4 /* a bounded wait for a TMA copy gave up */
 #define PRR_DEV_BAD_RANGE 5    /* summary update range outside [0, cap_tokens] or longer than max_range_tokens, or a block-table entry outside [0, pages) */
+#define PRR_DEV_NO_PAGES 6     /* prr_cache_reserve / prr_cache_fork: the pool has too few free pages (nothing was changed) */
 
 typedef struct {
   int32_t B;          /* sequences */
@@ -406,6 +407,129 @@ prr_status prr_select_topk_static(const prr_dims* dims, const uint16_t* q, const
                                   const int32_t* seq_lens, const int32_t* pred, int32_t* sel,
                                   int32_t* missed, int32_t* n_missed, uint8_t* keep,
                                   int32_t* status, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * Around the decode step: prompts and page tables.
+ *
+ * The calls below write a prompt's rows into the caches, attend it, let sequences share
+ * the pages of a paged cache, and attend a batch that shares prefixes.  They keep every
+ * convention above, with a workspace of their own: prr_serving_workspace_bytes sizes
+ * it, prr_workspace_init zeroes it, prr_get_device_status reads its status word.  Two
+ * calls that share a workspace must not overlap on the GPU (two captured graphs that
+ * share one included).  dims->K, P, alpha and the selector only have to be valid.
+ *
+ * Packed rows: the rows of several sequences stand one behind another, without padding;
+ * q_begin (device int32 [B+1], ascending) gives sequence b the rows [q_begin[b],
+ * q_begin[b+1]).  A sequence without rows takes no part; `rows` is the number of rows
+ * that the arrays hold, and rows from q_begin[B] on are neither read nor written.  A
+ * sequence whose range leaves [0, rows] sets PRR_DEV_BAD_RANGE and is skipped; where
+ * q_begin is not ascending, PRR_DEV_BAD_RANGE is set and the other sequences may be
+ * skipped too.  Rows may be part of wider ones: *_stride is the distance of two rows in elements, at least
+ * heads*d and a multiple of 8. */
+
+/* Bytes of workspace the calls of this section need for these dims and up to max_rows
+ * packed rows (0 if the dims are unsupported or max_rows is outside [1, 2^30]). */
+size_t prr_serving_workspace_bytes(const prr_dims* dims, int32_t max_rows);
+
+/* Append packed rows: k_rows / v_rows [rows][Hkv][d] bf16 of sequence b go to positions
+ * seq_lens[b], seq_lens[b]+1, ... of the caches; the summaries of the blocks they touch
+ * are extended (summ NULL: left alone), as prr_update_summaries does; then seq_lens[b]
+ * grows by the sequence's rows.  A sequence that would pass cap_tokens, or whose length
+ * is negative, sets PRR_DEV_BAD_SEQ_LEN and stays as it was.  A row whose block has no
+ * page (a table entry outside [0, pages)) is dropped and sets PRR_DEV_BAD_RANGE. */
+prr_status prr_append_prompt(const prr_dims* dims, const uint16_t* k_rows, const uint16_t* v_rows,
+                             int64_t row_stride, const int32_t* q_begin, int32_t rows,
+                             int32_t* seq_lens, uint16_t* k_cache, uint16_t* v_cache,
+                             uint16_t* summ, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Causal attention of packed prompt rows q [rows][Hq][d] bf16 over the caches, which
+ * hold the rows' own tokens already (prr_append_prompt): the l rows of sequence b are
+ * its newest l of seq_lens[b] tokens, and row i attends the tokens at positions
+ * 0 .. seq_lens[b]-l+i.  out [rows][Hq][d] bf16, lse [rows][Hq] fp32 (NULL: not
+ * written); only the sequences' rows are written.  A sequence with more rows than
+ * tokens, or a length outside [1, cap_tokens], sets PRR_DEV_BAD_SEQ_LEN and is skipped.
+ * Cache rows at or past seq_lens[b] may hold anything (NaN included); those below it are
+ * finite. */
+prr_status prr_attend_prompt(const prr_dims* dims, const uint16_t* q, int64_t q_stride,
+                             const int32_t* q_begin, int32_t rows, const int32_t* seq_lens,
+                             const uint16_t* k_cache, const uint16_t* v_cache, uint16_t* out,
+                             float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of one query per sequence, q [B][Hq][d] bf16, over ALL of its tokens, for a
+ * batch in groups that share a prefix: group g is members[group_begin[g] ..
+ * group_begin[g+1]) (device int32; group_begin [n_groups+1] ascending from 0,
+ * n_members <= B), and the first shared_blocks[g] blocks are the same for all of its
+ * members.  They are read once for the whole group, through its first member's rows of
+ * the cache (its part of the block table), and must be full: shared_blocks[g]*bs <=
+ * seq_lens of every member.  0 shares nothing.  out [B][Hq][d] bf16, lse [B][Hq] fp32
+ * (NULL: not written), written for the members only; a member of length 0 gets zeros and
+ * -infinity.  A member outside [0, B), a group whose range or shared_blocks is out of
+ * range for it (PRR_DEV_BAD_RANGE), or a length outside [0, cap_tokens]
+ * (PRR_DEV_BAD_SEQ_LEN) is skipped.  Two entries for one sequence both compute its row. */
+prr_status prr_attend_shared(const prr_dims* dims, const uint16_t* q, int64_t q_stride,
+                             const int32_t* members, int32_t n_members, const int32_t* group_begin,
+                             const int32_t* shared_blocks, int32_t n_groups, const int32_t* seq_lens,
+                             const uint16_t* k_cache, const uint16_t* v_cache, uint16_t* out,
+                             float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* What the prr_cache_* calls work on (paged caches, dims->pages > 0).  page_refs counts
+ * for every page the sequences whose table rows hold it; a page is free at 0.  A row
+ * holds its pages from block 0 on, and -1 in the blocks behind them.  A sequence's
+ * partly filled last page is always its own (prr_cache_fork copies it), so that appends
+ * never write a shared page. */
+typedef struct {
+  uint16_t* k_cache;    /* [pages][Hkv][bs][d] */
+  uint16_t* v_cache;
+  int32_t* block_table; /* [B][maxnb]; the same array as dims->block_table */
+  int32_t* page_refs;   /* [pages] */
+  int32_t* seq_lens;    /* [B] */
+  uint16_t* summ;       /* NULL: none kept */
+  double* ema;          /* NULL: none kept */
+  int32_t* pred;        /* Pred_t; NULL: none kept */
+  uint8_t* rep_offsets; /* NULL: none kept */
+} prr_cache_buffers;
+
+/* Make room: sequence b gets pages for the blocks below want_lens[b] tokens (device int32
+ * [B]) that its row does not hold; the blocks below seq_lens[b] are taken as held.  Pages
+ * are the lowest free ones, given out in the order of (sequence, block).  Too few free
+ * pages set PRR_DEV_NO_PAGES and change nothing; want_lens[b] above cap_tokens sets
+ * PRR_DEV_BAD_SEQ_LEN and skips that sequence.  Needs block_table, page_refs and
+ * seq_lens. */
+prr_status prr_cache_reserve(const prr_dims* dims, const int32_t* want_lens,
+                             const prr_cache_buffers* cache, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* Fork: for i < n, sequence children[i] (empty: length 0, no pages) becomes a copy of
+ * parents[i] as it is before the call (device int32 [n]).  Full blocks share the
+ * parent's pages; a partly filled last block is copied into the lowest free page, in the
+ * order of i; pages that the parent holds beyond its length stay its own.  Summaries,
+ * representative offsets and EMA entries of the parent's blocks and its prediction are
+ * copied where the buffers are given; EMA entries behind them become 0.  A child that is
+ * not empty, an index outside [0, B), and all but the first of several entries for one
+ * child set PRR_DEV_BAD_RANGE and are skipped; too few free pages set PRR_DEV_NO_PAGES
+ * and change nothing.  n <= B.  Needs all buffers but the last four. */
+prr_status prr_cache_fork(const prr_dims* dims, const int32_t* parents, const int32_t* children,
+                          int32_t n, const prr_cache_buffers* cache, void* ws, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/* Release the sequences seqs[0..n) (device int32, n <= B): their pages lose one reference
+ * each, their table rows become -1, their lengths 0, and where the buffers are given
+ * their EMA state 0 and their prediction that of the zero state (blocks 0 .. P-1), so
+ * that the slot can take another sequence.  A second entry for a sequence does nothing;
+ * an index outside [0, B), a table entry outside the pool and a page whose count is 0
+ * already set PRR_DEV_BAD_RANGE.  Needs block_table, page_refs and seq_lens. */
+prr_status prr_cache_release(const prr_dims* dims, const int32_t* seqs, int32_t n,
+                             const prr_cache_buffers* cache, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* Compact the pool: with L live pages (page_refs > 0), the live pages at L and above move,
+ * in ascending order, into the free ones below L, in ascending order, so that the pool's
+ * first L pages are the live ones.  Rows of K and V are copied, table entries and counts
+ * follow.  remap (device int32 [pages]) receives each page's new place, -1 for a free
+ * one; n_live (device int32) receives L.  Needs k_cache, v_cache, block_table and
+ * page_refs. */
+prr_status prr_cache_compact(const prr_dims* dims, const prr_cache_buffers* cache, int32_t* remap,
+                             int32_t* n_live, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
