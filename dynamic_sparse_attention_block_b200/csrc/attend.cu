@@ -1,121 +1,860 @@
 // attend.cu -- dense attention over the caches: packed causal prompts, and a batch in
 // groups that share prefixes.
 //
-// Per query row q and head: s_j = scale * q . k_j over its tokens j, out = sum_j softmax(s)_j v_j,
-// lse = log sum_j exp(s_j).  This is the plain kernel: one warp per (row, query head),
-// 32 tokens at a time with the running maximum and sum of the softmax (one token per lane
-// for q . k, d/32 channels per lane for the sum over v).
+// Per query row and head: s_j = scale * q . k_j over its tokens j,
+//   out = sum_j 2^(s'_j - m) v_j / sum_j 2^(s'_j - m),   lse = (m + log2 sum) ln 2,   s' = s log2 e,
+// in one pass over the tokens with a running reference m (tensor cores for both products).
+//
+// Tiles.  A tile is up to 256 rows that read the same tokens of one KV head: the G query
+// heads of its group times up to 2 * floor(128/G) packed tokens of one prompt, or the G heads of
+// that many members of a group (over the shared prefix) or of one sequence (over its own
+// tokens).  It is attended in blocks of 128 tokens; a tile's weight is its number of
+// blocks.  The plan kernel numbers all (head, tile, block) units and cuts them into
+// equal runs, one per CTA, wherever the cuts fall -- so prompts, single tokens, long
+// prefixes and ragged batches all fill the machine evenly.  A tile cut between CTAs (and every
+// tile of a batch in groups) leaves fp32 partials (m, sum, O) that combine kernels merge.
+//
+// A CTA (one per SM) runs, per tile piece: one thread that issues the TMA copies of K and
+// V blocks through a ring of stages; one that issues the products; and two groups of 128
+// threads, one per 128 rows, each thread owning one row.  For rows t in {0, 1}:
+//   S_t = Q_t K^T (tensor memory), softmax group t turns S_t into P_t = 2^(s' - m) in place,
+//   O_t += P_t V (tensor memory), with S of one half and the softmax of the other overlapping.
+// P is rounded to bf16 (the product's operand type): half a step, 2^-8 of each weight at most; its sum,
+// m and O stay fp32.  m only moves when a row's maximum grew by more than 2^8: until then weights up
+// to 256 are exact in range, and O needs no rescaling.
 #include "prr_serving.cuh"
+#include "prr_tensor.cuh"
 
 namespace prr {
 
 namespace {
 
-template <int D>
-__global__ void attend_rows_kernel(const __grid_constant__ Params p, const __grid_constant__ AttendArgs a) {
-  const int lane = threadIdx.x & 31, h = blockIdx.y, hq = h * p.G + (threadIdx.x >> 5);
-  const bool tell = threadIdx.x == 0 && h == 0;
-  int seq, first, shared_to = 0, row, n;  // tokens [0, n); below shared_to through `first`
-  if (a.q_begin) {
-    row = blockIdx.x;
-    int lo = 0, hi = p.B - 1;
+constexpr int kBlock = 128;         // tokens per step
+constexpr float kGrow = 8.0f;       // log2 of the growth that moves the reference m
+constexpr int kPlanThreads = 1024;
+constexpr int kAttendThreads = 320;  // 2 x 128 softmax threads, a product warp, a copy warp
+constexpr int kCombineRows = 64;
+
+__host__ __device__ constexpr int sub_tokens(int G) { return kBlock / G; }  // packed tokens per 128 rows
+
+struct Tile {  // 32 bytes
+  int row0;    // first entry of the row list
+  int ntok;    // packed tokens (each G rows)
+  int seq;     // whose tokens it reads
+  int kv0;     // first token
+  int kv1;     // one past the last
+  int pos0;    // causal: position of the first packed token; kNoMask: every row reads all of [kv0, kv1)
+  int blocks;  // weight
+  int part0;   // first row of its partials (batch in groups)
+};
+constexpr int kNoMask = 1 << 30;
+
+struct Start {  // where a CTA's run begins
+  int head, tile, off, pad;
+};
+
+struct PlanHead {
+  long long per_head;  // units of one KV head
+  int tiles;
+  int ctas;            // CTAs with work
+};
+
+struct Plan {
+  PlanHead* head;
+  Start* start;        // [kMaxAttendCtas + 1]
+  long long* prefix;   // [tiles + 1] units before each tile
+  Tile* tile;
+  int* row;            // [B] batch in groups: the sequence of each entry, -1: skipped
+  float* part;         // partial rows: m, sum, O[d]
+};
+
+__host__ __device__ inline long long first_unit(long long units, int ctas, int c) { return units * c / ctas; }
+
+// ------------------------------------------------------------------ the plan
+
+template <typename T>
+__device__ T plan_scan(T v, T* total) {  // exclusive prefix sum over the CTA
+  __shared__ T warp_sum[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    T s = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sum[lane] = s;
+  }
+  __syncthreads();
+  *total = warp_sum[kPlanThreads / 32 - 1];
+  return x - v + (w ? warp_sum[w - 1] : 0);
+}
+
+// Tile `slot` of packed prompts.  Sequence b owns the slots floor(q_begin[b] / span) + b
+// ...: at least as many as it has tiles, so a slot finds its tile by bisection; slots left over weigh 0.
+__device__ Tile prompt_tile(const Params& p, const AttendArgs& a, int slot, int span) {
+  Tile t = {};
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (max(a.q_begin[mid], 0) / span + mid <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  const int j = slot - (max(a.q_begin[lo], 0) / span + lo);
+  int r0, r1;
+  if (!packed_range(a.q_begin, lo, a.rows, &r0, &r1, p.status, true) || j < 0) return t;
+  if (j >= (r1 - r0 + span - 1) / span) return t;
+  const int len = p.seq_lens[lo];
+  if (len < 1 || len > p.cap || r1 - r0 > len) {
+    report(p.status, kDevBadSeqLen);
+    return t;
+  }
+  t.row0 = r0 + j * span;
+  t.ntok = min(span, r1 - t.row0);
+  t.seq = lo;
+  t.pos0 = len - (r1 - r0) + j * span;
+  t.kv1 = t.pos0 + t.ntok;
+  t.blocks = (t.kv1 + kBlock - 1) / kBlock;
+  return t;
+}
+
+// What entry i of a batch in groups is: its group, whether it takes part.
+struct Entry {
+  int g, g0, g1, first, seq, n, shared;
+};
+
+__device__ bool group_entry(const Params& p, const AttendArgs& a, int i, Entry* e) {
+  int lo = 0, hi = a.n_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.group_begin[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  e->g = lo;
+  e->g0 = a.group_begin[lo];
+  e->g1 = a.group_begin[lo + 1];
+  const int sb = a.shared_blocks[lo];
+  if (e->g1 == e->g0 || i >= e->g1) {
+    if (e->g1 < e->g0) report(p.status, kDevBadRange);
+    return false;  // entries behind the last group take no part
+  }
+  if (e->g0 < 0 || e->g0 > i || e->g1 > a.n_members || sb < 0 || sb > p.maxnb) {
+    report(p.status, kDevBadRange);
+    return false;
+  }
+  e->seq = a.members[i];
+  e->first = a.members[e->g0];
+  if (e->seq < 0 || e->seq >= p.B || e->first < 0 || e->first >= p.B) {
+    report(p.status, kDevBadRange);
+    return false;
+  }
+  e->n = p.seq_lens[e->seq];
+  const int fn = sb > 0 ? p.seq_lens[e->first] : e->n;  // the prefix is read through the first member
+  if (e->n < 0 || e->n > p.cap || fn < 0 || fn > p.cap) {
+    report(p.status, kDevBadSeqLen);
+    return false;
+  }
+  const long long shared = static_cast<long long>(sb) * p.bs;
+  if (shared > e->n || shared > fn) {
+    report(p.status, kDevBadRange);
+    return false;
+  }
+  e->shared = static_cast<int>(shared);
+  return true;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ Params p,
+                                                            const __grid_constant__ AttendArgs a,
+                                                            const __grid_constant__ Plan plan, int slots, int max_ctas) {
+  const int span = 2 * sub_tokens(p.G);
+  long long sum = 0;
+  for (int base = 0; base < slots; base += kPlanThreads) {
+    const int slot = base + threadIdx.x;
+    Tile t = {};
+    if (slot < slots) {
+      if (a.q_begin) {
+        t = prompt_tile(p, a, slot, span);
+      } else if (slot < a.n_members) {  // own tokens of entry `slot`
+        Entry e;
+        const bool ok = group_entry(p, a, slot, &e);
+        plan.row[slot] = ok ? e.seq : -1;
+        if (ok && e.n > e.shared) {
+          t.row0 = slot;
+          t.ntok = 1;
+          t.seq = e.seq;
+          t.kv0 = e.shared;
+          t.kv1 = e.n;
+          t.pos0 = kNoMask;
+          t.blocks = (t.kv1 - t.kv0 + kBlock - 1) / kBlock;
+          t.part0 = (a.n_members + slot) * p.Hq;
+        }
+      } else {  // shared prefix: the slot of the entry that leads `span` entries of its group
+        const int i = slot - a.n_members;
+        Entry e;
+        // an entry that takes no part itself still leads the others
+        int lo = 0, hi = a.n_groups - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (a.group_begin[mid] <= i) lo = mid;
+          else hi = mid - 1;
+        }
+        const int g0 = a.group_begin[lo], g1 = a.group_begin[lo + 1], sb = a.shared_blocks[lo];
+        if (g0 >= 0 && g0 <= i && i < g1 && g1 <= a.n_members && sb > 0 && sb <= p.maxnb && (i - g0) % span == 0) {
+          const int first = a.members[g0];
+          if (first >= 0 && first < p.B && group_entry(p, a, g0, &e)) {
+            t.row0 = i;
+            t.ntok = min(span, g1 - i);
+            t.seq = first;
+            t.kv1 = sb * p.bs;
+            t.pos0 = kNoMask;
+            t.blocks = (t.kv1 + kBlock - 1) / kBlock;
+            t.part0 = i * p.Hq;
+          }
+        }
+      }
+      plan.tile[slot] = t;
+    }
+    long long total;
+    const long long at = sum + plan_scan<long long>(t.blocks, &total);
+    if (slot < slots) plan.prefix[slot] = at;
+    sum += total;
+  }
+  if (threadIdx.x == 0) plan.prefix[slots] = sum;
+  __syncthreads();
+  const long long units = sum * p.Hkv;
+  const int ctas = static_cast<int>(min(static_cast<long long>(max_ctas), units));
+  if (threadIdx.x == 0) *plan.head = PlanHead{sum, slots, ctas};
+  for (int c = threadIdx.x; c < ctas; c += kPlanThreads) {
+    const long long g = first_unit(units, ctas, c);
+    const int head = static_cast<int>(g / sum);
+    const long long r = g - head * sum;
+    int lo = 0, hi = slots - 1;  // the last tile that begins at or before r: not an empty one
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.q_begin[mid] <= row) lo = mid;
+      if (plan.prefix[mid] <= r) lo = mid;
       else hi = mid - 1;
     }
-    first = seq = lo;
-    int r0, r1;
-    if (!packed_range(a.q_begin, seq, a.rows, &r0, &r1, p.status, tell) || row < r0 || row >= r1) return;
-    const int len = p.seq_lens[seq];
-    if (len < 1 || len > p.cap || r1 - r0 > len) {
-      if (tell) report(p.status, kDevBadSeqLen);
-      return;
+    plan.start[c] = Start{head, lo, static_cast<int>(r - plan.prefix[lo]), 0};
+  }
+}
+
+// ------------------------------------------------------------------ walking a CTA's run
+
+struct Piece {
+  Tile t;
+  int head;
+  int b0, b1;   // blocks of the tile
+  bool whole;   // this CTA has all of the tile
+  bool first;   // ... has its first block
+};
+
+struct Walk {
+  const Plan* plan;
+  long long left;
+  int head, tile, off;
+
+  __device__ Walk(const Plan& pl, int kv_heads, int c) : plan(&pl) {
+    const PlanHead h = *pl.head;
+    left = 0;
+    if (c < h.ctas) {
+      const long long units = h.per_head * kv_heads;
+      left = first_unit(units, h.ctas, c + 1) - first_unit(units, h.ctas, c);
+      const Start s = pl.start[c];
+      head = s.head;
+      tile = s.tile;
+      off = s.off;
     }
-    n = len - (r1 - r0) + (row - r0) + 1;
+  }
+
+  __device__ bool next(Piece* x) {
+    while (left > 0) {
+      x->t = plan->tile[tile];
+      const int take = static_cast<int>(min(left, static_cast<long long>(x->t.blocks - off)));
+      x->head = head;
+      x->b0 = off;
+      x->b1 = off + take;
+      x->first = off == 0;
+      x->whole = take == x->t.blocks;
+      left -= take;
+      off = 0;
+      if (++tile == plan->head->tiles) {
+        tile = 0;
+        ++head;
+      }
+      if (take > 0) return true;
+    }
+    return false;
+  }
+};
+
+// ------------------------------------------------------------------ the attention kernel
+
+template <int D>
+struct Smem {
+  static constexpr int TILE = kBlock * D * 2;  // one Q, K or V tile
+  static constexpr int SLAB = kBlock * 128;    // one 64-channel slab of it
+  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int Q = 0;
+  static constexpr int KV = 2 * TILE;
+  static constexpr int BARS = KV + STAGES * TILE;
+  static constexpr int BYTES = BARS + 256;
+};
+
+struct Bars {
+  uint64_t full[10], empty[10];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barriers fit behind the stages");
+
+// Bounded wait of the kernel's roles, by whole warps; one that gives up makes all give up.
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t phase, volatile int* abort, int* status) {
+  bool ok = mbar_try_wait(bar, phase);
+  if (__all_sync(0xFFFFFFFFu, ok)) return true;
+  const uint64_t t0 = global_ns();
+  while (!ok) {
+    ok = mbar_try_wait(bar, phase);
+    if (ok || *abort) break;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      report(status, kDevWaitTimeout);
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+template <int D, int BS>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ Params p, const __grid_constant__ AttendArgs a,
+                  const __grid_constant__ Plan plan) {
+  using L = Smem<D>;
+  constexpr int NS = L::STAGES, NREG = D / 64, HALVES = kBlock / BS;
+  constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars& bars = *reinterpret_cast<Bars*>(smem + L::BARS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.G, tps = sub_tokens(G);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.q_full[t], 128);
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.o_full[t], 1);
+      mbar_init(&bars.o_free[t], 128);
+    }
+    mbar_init(&bars.drain, 1);
+    bars.abort = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  if (warp == 8) {
+    tmem_alloc(&bars.tmem, TMEM_COLS);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  volatile int* abort = &bars.abort;
+  Walk walk(plan, p.Hkv, blockIdx.x);
+  Piece x;
+
+  if (warp == 9) {
+    // ---------------------------------------------------------------- copies
+    int s = 0;
+    uint32_t ph = 0;      // phase of the ring: stage s has been filled ph times (mod 2)
+    long long fills = 0;  // copies issued, in stages
+    bool ok = true;
+    while (ok && walk.next(&x)) {
+      int page = 0, have = -1;  // lane i: the page of cache block have + i
+      for (int b = x.b0; ok && b < x.b1; ++b) {
+        const int t0 = x.t.kv0 + b * kBlock;
+        int slice[2], tok[2], n = 0;
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+          const int th = t0 + hf * BS;
+          if (th < x.t.kv1) {
+            n = hf + 1;
+            if (p.table) {
+              const int blk = th / BS;
+              if (have < 0 || blk >= have + 32) {
+                have = blk;
+                page = blk + lane < (x.t.kv1 + BS - 1) / BS
+                           ? p.table[static_cast<size_t>(x.t.seq) * p.maxnb + blk + lane] : 0;
+              }
+              const int pg = __shfl_sync(0xFFFFFFFFu, page, blk - have);
+              const bool good = pg >= 0 && pg < p.pages;
+              if (!good && lane == 0) report(p.status, kDevBadRange);
+              slice[hf] = good ? pg * p.Hkv + x.head : p.pages * p.Hkv;  // past the map: zeros
+              tok[hf] = 0;
+            } else {
+              slice[hf] = x.t.seq * p.Hkv + x.head;
+              tok[hf] = th;
+            }
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && role_wait(&bars.empty[s], ph ^ 1, abort, p.status);
+          if (ok && lane == 0) {
+            unsigned char* dst = smem + L::KV + s * L::TILE;
+            mbar_expect_tx(&bars.full[s], n * BS * D * 2);
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+              if (hf < n)
+#pragma unroll
+                for (int r = 0; r < NREG; ++r)
+                  tma_load_3d(dst + r * L::SLAB + hf * BS * 128, kv ? &vmap : &kmap, &bars.full[s], r * 64, tok[hf],
+                              slice[hf]);
+          }
+          if (ok) ++fills;
+          if (ok && ++s == NS) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    // copies still in flight land before the CTA ends (all have, unless a wait ran out)
+    if (*abort && lane == 0)
+      for (long long f = max(0ll, fills - NS); f < fills; ++f)
+        mbar_wait(&bars.full[f % NS], static_cast<uint32_t>(f / NS) & 1, p.status);
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t QK = mma_desc(128, 128, false), PV = mma_desc(128, D, true);
+    const uint32_t sQ = smem_addr(smem + L::Q), sKV = smem_addr(smem + L::KV);
+    uint32_t qph = 0, pph = 0, oph = 0;  // phases, bit t for rows t
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto qk = [&](int t, int stage) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = (k / 4) * L::SLAB + (k % 4) * 32;
+        mma_ss(tmem + S_COL + t * 128, tile_desc(sQ + t * L::TILE + at, 16, 1024),
+               tile_desc(sKV + stage * L::TILE + at, 16, 1024), QK, k > 0);
+      }
+    };
+    while (ok && walk.next(&x)) {
+      const int halves = x.t.ntok > tps ? 2 : 1;
+      for (int t = 0; ok && t < halves; ++t) {
+        ok = role_wait(&bars.q_full[t], (qph >> t) & 1, abort, p.status);
+        qph ^= 1u << t;
+      }
+      ok = ok && role_wait(&bars.full[s], ph, abort, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        for (int t = 0; t < halves; ++t) {
+          qk(t, s);
+          tc_commit(&bars.s_full[t]);
+        }
+        tc_commit(&bars.empty[s]);
+      }
+      if (++s == NS) {
+        s = 0;
+        ph ^= 1;
+      }
+      for (int b = x.b0; ok && b < x.b1; ++b) {
+        const int vs = s;
+        const uint32_t vph = ph;
+        if (++s == NS) {
+          s = 0;
+          ph ^= 1;
+        }
+        const bool more = b + 1 < x.b1;
+        for (int t = 0; ok && t < halves; ++t) {
+          if (t == 0) {
+            ok = role_wait(&bars.full[vs], vph, abort, p.status);
+            const int valid = x.t.kv1 - (x.t.kv0 + b * kBlock);
+            if (ok && valid < kBlock) {  // rows past the last token may hold anything: 0 * NaN is not 0
+              for (int i = valid * 8 + lane; i < kBlock * 8; i += 32)
+#pragma unroll
+                for (int r = 0; r < NREG; ++r)
+                  *reinterpret_cast<uint4*>(smem + L::KV + vs * L::TILE + r * L::SLAB + i * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async();
+              __syncwarp();
+            }
+          }
+          ok = ok && role_wait(&bars.p_full[t], (pph >> t) & 1, abort, p.status);
+          pph ^= 1u << t;
+          if (ok && b == x.b0) {  // the previous piece's O has been read
+            ok = role_wait(&bars.o_free[t], ((oph >> t) & 1) ^ 1, abort, p.status);
+            oph ^= 1u << t;
+          }
+          if (ok && more && t == 0) ok = role_wait(&bars.full[s], ph, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+              mma_ts(tmem + O_COL + t * D, tmem + S_COL + t * 128 + k * 8,
+                     tile_desc(sKV + vs * L::TILE + k * 2048, L::SLAB, 1024), PV, b > x.b0 || k > 0);
+            if (more) {
+              qk(t, s);
+              tc_commit(&bars.s_full[t]);
+            } else {
+              tc_commit(&bars.o_full[t]);
+            }
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          tc_commit(&bars.empty[vs]);
+          if (more) tc_commit(&bars.empty[s]);
+        }
+        if (more && ++s == NS) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+    if (*abort && lane == 0) {  // products still in flight end before their memory is given back
+      tc_commit(&bars.drain);
+      mbar_wait(&bars.drain, 0, p.status);
+    }
+    __syncwarp();
   } else {
-    const int i = blockIdx.x;
+    // ---------------------------------------------------------------- softmax, rows t
+    const int t = warp >> 2, tid = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + S_COL + t * 128 + lanes, tO = tmem + O_COL + t * D + lanes;
+    uint32_t sph = 0, oph = 0;
+    // a negative scale changes q's signs, so that the largest product has the largest logit; scale 0 is q = 0
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
+    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    bool ok = true;
+    while (ok && walk.next(&x)) {
+      const int ntok = min(tps, x.t.ntok - t * tps);
+      if (ntok <= 0) continue;
+      // rows of Q, swizzled as the products read them
+      for (int i = tid; i < kBlock * (D / 8); i += 128) {
+        const int r = i / (D / 8), c = i % (D / 8), tok = r / G;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (tok < ntok) {
+          const int e = x.t.row0 + t * tps + tok;
+          const int row = a.q_begin ? e : plan.row[e];
+          if (row >= 0)
+            w = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * a.q_stride +
+                                                     static_cast<size_t>(x.head * G + r % G) * D + c * 8));
+          w.x = (w.x ^ flip) & keep;
+          w.y = (w.y ^ flip) & keep;
+          w.z = (w.z ^ flip) & keep;
+          w.w = (w.w ^ flip) & keep;
+        }
+        *reinterpret_cast<uint4*>(smem + L::Q + t * L::TILE + (c >> 3) * L::SLAB + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
+      }
+      fence_proxy_async();
+      mbar_arrive(&bars.q_full[t]);
+
+      const int tok = tid / G;
+      const bool mine = tok < ntok;
+      const bool work = __any_sync(0xFFFFFFFFu, mine);
+      const int e = x.t.row0 + t * tps + (mine ? tok : 0);
+      const int row = !mine ? -1 : a.q_begin ? e : plan.row[e];
+      // one past the last token this row reads; rows of no one read all
+      const int end = !mine ? kNoMask : x.t.pos0 == kNoMask ? x.t.kv1 : x.t.pos0 + t * tps + tok + 1;
+      float m = -INFINITY, sum = 0.f;
+      for (int b = x.b0; ok && b < x.b1; ++b) {
+        ok = role_wait(&bars.s_full[t], sph, abort, p.status);
+        sph ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        if (work) {
+          uint32_t s[kBlock];
+#pragma unroll
+          for (int c = 0; c < kBlock; c += 32) tmem_ld32(tS + c, s + c);
+          tmem_wait_ld();
+          const int lim = end - (x.t.kv0 + b * kBlock);
+          if (__any_sync(0xFFFFFFFFu, lim < kBlock)) {
+#pragma unroll
+            for (int c = 0; c < kBlock; ++c)
+              if (c >= lim) s[c] = 0xFF800000u;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kBlock; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
+          const float m1 = fmaxf(m, mx * scale);
+          if (b == x.b0) {
+            m = m1;
+          } else if (__any_sync(0xFFFFFFFFu, m1 - m > kGrow || (m == -INFINITY && m1 > m))) {
+            const float f = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
+            m = m1;
+            sum *= f;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(tO + c, o);
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          float part = 0.f;
+#pragma unroll
+          for (int c = 0; c < kBlock; c += 2) {
+            const float w0 = exp2_fast(fmaf(__uint_as_float(s[c]), scale, -base));
+            const float w1 = exp2_fast(fmaf(__uint_as_float(s[c + 1]), scale, -base));
+            part += w0 + w1;
+            s[c / 2] = pack_bf16(w0, w1);
+          }
+          sum += part;
+          tmem_st32(tS, s);
+          tmem_st32(tS + 32, s + 32);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[t]);
+      }
+      ok = ok && role_wait(&bars.o_full[t], oph, abort, p.status);
+      oph ^= 1;
+      if (!ok) break;
+      tc_fence_after();
+      if (work) {
+        const int hq = x.head * G + tid % G;
+        const bool direct = a.q_begin && x.whole;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const size_t at = static_cast<size_t>(row < 0 ? 0 : row) * p.Hq + hq;
+        // partial rows: of the CTA (a tile's later pieces; of a prompt also its first), or of the batch
+        const size_t prow = !x.first ? (2ull * blockIdx.x) * 256 + t * kBlock + tid
+                            : a.q_begin ? (2ull * blockIdx.x + 1) * 256 + t * kBlock + tid
+                                        : 2ull * kMaxAttendCtas * 256 + x.t.part0 +
+                                              static_cast<size_t>(t * tps + tok) * p.Hq + hq;
+        float* part = plan.part + prow * (D + 4);
+        if (row >= 0 && direct) {
+          if (a.lse) a.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
+        } else if (row >= 0) {
+          part[0] = m;
+          part[1] = sum;
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
+          if (row >= 0 && direct) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+              w.y = pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+              w.z = pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+              w.w = pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+              *reinterpret_cast<uint4*>(a.out + at * D + c + i) = w;
+            }
+          } else if (row >= 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(part + 4 + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars.o_free[t]);
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ merging partials
+
+// Merge the n partial rows that row_of(i) names and write the result; one warp.
+template <int D, typename RowOf>
+__device__ void merge_rows(const Plan& plan, const AttendArgs& a, int n, size_t at, RowOf row_of) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, plan.part[row_of(i) * (D + 4)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float sum = 0.f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const float* r = plan.part + row_of(i) * (D + 4);
+    const float f = r[0] == -INFINITY ? 0.f : exp2f(r[0] - m);
+    sum += r[1] * f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += r[4 + lane * C + c] * f;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint32_t w[C / 2];
+#pragma unroll
+  for (int c = 0; c < C; c += 2) w[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+#pragma unroll
+  for (int c = 0; c < C / 2; ++c) reinterpret_cast<uint32_t*>(a.out + at * D + lane * C)[c] = w[c];
+  if (a.lse && lane == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The CTAs that have units [z0, z1): [*c0, *c1].
+__device__ __forceinline__ void ctas_of(long long units, int ctas, long long z0, long long z1, int* c0, int* c1) {
+  int lo = static_cast<int>(z0 * ctas / units);
+  while (lo + 1 < ctas && first_unit(units, ctas, lo + 1) <= z0) ++lo;
+  int hi = lo;
+  while (hi + 1 < ctas && first_unit(units, ctas, hi + 1) < z1) ++hi;
+  *c0 = lo;
+  *c1 = hi;
+}
+
+// Packed prompts: CTA column c merges the tile that was cut first at the start of CTA c's run.
+template <int D>
+__global__ void __launch_bounds__(256) combine_tiles_kernel(const __grid_constant__ Params p,
+                                                            const __grid_constant__ AttendArgs a,
+                                                            const __grid_constant__ Plan plan) {
+  const int c = blockIdx.x + 1;
+  const PlanHead h = *plan.head;
+  if (c >= h.ctas) return;
+  const Start s = plan.start[c];
+  if (s.off == 0) return;
+  const long long units = h.per_head * p.Hkv;
+  const Tile t = plan.tile[s.tile];
+  const long long z0 = first_unit(units, h.ctas, c) - s.off;
+  if (first_unit(units, h.ctas, c - 1) > z0) return;  // an earlier column has this tile
+  int last = c;
+  while (last + 1 < h.ctas && first_unit(units, h.ctas, last + 1) < z0 + t.blocks) ++last;
+  const int tps = sub_tokens(p.G), n = last - c + 2;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < t.ntok * p.G; r += gridDim.y * 8) {
+    const int tok = r / p.G, g = r % p.G;
+    const int prow = tok / tps * kBlock + (tok % tps) * p.G + g;
+    const size_t at = static_cast<size_t>(t.row0 + tok) * p.Hq + s.head * p.G + g;
+    merge_rows<D>(plan, a, n, at, [&](int i) {
+      return (i == 0 ? 2ull * (c - 1) + 1 : 2ull * (c + i - 1)) * 256 + prow;
+    });
+  }
+}
+
+// A batch in groups: one warp per (entry, query head) merges its prefix and its own tokens.
+template <int D>
+__global__ void __launch_bounds__(256) combine_entries_kernel(const __grid_constant__ Params p,
+                                                              const __grid_constant__ AttendArgs a,
+                                                              const __grid_constant__ Plan plan) {
+  const int i = blockIdx.x, head = blockIdx.y, g = threadIdx.x >> 5;
+  const int row = plan.row[i];
+  if (row < 0) return;
+  const PlanHead h = *plan.head;
+  const long long units = h.per_head * p.Hkv;
+  const int tps = sub_tokens(p.G), hq = head * p.G + g;
+  int c0[2] = {0, 0}, n[2] = {0, 0};
+  size_t first[2], later[2];
+  // the entry's own tile, and the prefix tile that leads it
+  int lead = -1;
+  {
     int lo = 0, hi = a.n_groups - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (a.group_begin[mid] <= i) lo = mid;
       else hi = mid - 1;
     }
-    const int g0 = a.group_begin[lo], g1 = a.group_begin[lo + 1], sb = a.shared_blocks[lo];
-    if (g0 < 0 || g0 > i || g1 <= i || g1 > a.n_members || sb < 0 || sb > p.maxnb) {
-      if (tell && g1 != g0) report(p.status, kDevBadRange);
-      return;
-    }
-    seq = row = a.members[i];
-    first = a.members[g0];
-    if (seq < 0 || seq >= p.B || first < 0 || first >= p.B) {
-      if (tell) report(p.status, kDevBadRange);
-      return;
-    }
-    n = p.seq_lens[seq];
-    if (n < 0 || n > p.cap) {
-      if (tell) report(p.status, kDevBadSeqLen);
-      return;
-    }
-    shared_to = sb * p.bs;
-    if (shared_to > n) {
-      if (tell) report(p.status, kDevBadRange);
-      return;
-    }
+    const int g0 = a.group_begin[lo];
+    lead = i - (i - g0) % (2 * tps);
   }
+  const int slot[2] = {a.n_members + lead, i};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Tile t = plan.tile[slot[k]];
+    if (t.blocks == 0) continue;
+    const long long z0 = head * h.per_head + plan.prefix[slot[k]];
+    int c1;
+    ctas_of(units, h.ctas, z0, z0 + t.blocks, &c0[k], &c1);
+    n[k] = c1 - c0[k] + 1;
+    const int tok = i - t.row0;
+    first[k] = 2ull * kMaxAttendCtas * 256 + t.part0 + static_cast<size_t>(tok) * p.Hq + hq;
+    later[k] = tok / tps * kBlock + (tok % tps) * p.G + g;
+  }
+  merge_rows<D>(plan, a, n[0] + n[1], static_cast<size_t>(row) * p.Hq + hq, [&](int j) {
+    const int k = j < n[0] ? 0 : 1, piece = k ? j - n[0] : j;
+    return piece == 0 ? first[k] : 2ull * (c0[k] + piece) * 256 + later[k];
+  });
+}
 
-  constexpr int C = D / 32;  // channels per lane
-  const uint16_t* q = a.q + static_cast<size_t>(row) * a.q_stride + static_cast<size_t>(hq) * D;
-  float m = -INFINITY, l = 0.f, o[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = 0.f;
-  for (int t0 = 0; t0 < n; t0 += 32) {  // a tile of 32 tokens lies in one block
-    const long long r = kv_row(p, (t0 < shared_to ? first : seq) * p.Hkv + h, t0);
-    if (r < 0) continue;
-    float s = -INFINITY;
-    if (t0 + lane < n) {
-      const uint4* kr = reinterpret_cast<const uint4*>(p.kc + static_cast<size_t>(r + lane) * D);
-      s = 0.f;
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 kw = kr[c], qw = reinterpret_cast<const uint4*>(q)[c];
-        const uint32_t kk[4] = {kw.x, kw.y, kw.z, kw.w}, qq[4] = {qw.x, qw.y, qw.z, qw.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s += bf16_lo(kk[e]) * bf16_lo(qq[e]) + bf16_hi(kk[e]) * bf16_hi(qq[e]);
-      }
-      s *= p.scale_log2;
-    }
-    float mt = s;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, x));
-    const float mn = fmaxf(m, mt), base = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - base), w = exp2f(s - base);
-    float ws = w;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) ws += __shfl_xor_sync(0xFFFFFFFFu, ws, x);
-    l = l * f + ws;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] *= f;
-    for (int t = 0; t < min(32, n - t0); ++t) {
-      const float wt = __shfl_sync(0xFFFFFFFFu, w, t);
-      const uint16_t* vr = p.vc + static_cast<size_t>(r + t) * D + lane * C;
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += wt * __uint_as_float(static_cast<uint32_t>(vr[i]) << 16);
-    }
+// ------------------------------------------------------------------ launches
+
+Plan plan_of(const Params& p, const AttendArgs& a) {
+  unsigned char* w = static_cast<unsigned char*>(a.work);
+  Plan plan;
+  const size_t tiles = attend_tiles(p.B, a.max_rows, p.G);
+  auto take = [&](size_t bytes) {
+    unsigned char* at = w;
+    w += (bytes + 255) & ~static_cast<size_t>(255);
+    return at;
+  };
+  plan.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
+  plan.start = reinterpret_cast<Start*>(take(sizeof(Start) * kMaxAttendCtas));
+  plan.prefix = reinterpret_cast<long long*>(take(8 * (tiles + 1)));
+  plan.tile = reinterpret_cast<Tile*>(take(sizeof(Tile) * tiles));
+  plan.row = reinterpret_cast<int*>(take(4 * static_cast<size_t>(p.B)));
+  plan.part = reinterpret_cast<float*>(w);
+  return plan;
+}
+
+template <int D, int BS>
+cudaError_t launch_attend_t(const Params& p, const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                            int sms, cudaStream_t s) {
+  const Plan plan = plan_of(p, a);
+  const int span = 2 * sub_tokens(p.G);
+  const int slots = a.q_begin ? a.rows / span + p.B : 2 * a.n_members;
+  const int ctas = sms < kMaxAttendCtas ? sms : kMaxAttendCtas;
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(attend_kernel<D, BS>));
+  if (e == cudaSuccess) e = launch_kernel(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, 0, p, a, plan, slots, ctas);
+  if (e == cudaSuccess)
+    e = launch_kernel(attend_kernel<D, BS>, dim3(ctas), dim3(kAttendThreads), Smem<D>::BYTES + 1024, s, 0, kmap, vmap, p,
+                      a, plan);
+  if (e != cudaSuccess) return e;
+  if (a.q_begin) {
+    if (ctas == 1) return e;
+    return launch_kernel(combine_tiles_kernel<D>, dim3(ctas - 1, 256 / kCombineRows * 2), dim3(256), 0, s, 0, p, a, plan);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t at = static_cast<size_t>(row) * p.Hq + hq;
-#pragma unroll
-  for (int i = 0; i < C; ++i) reinterpret_cast<__nv_bfloat16*>(a.out)[at * D + lane * C + i] = __float2bfloat16(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return launch_kernel(combine_entries_kernel<D>, dim3(a.n_members, p.Hkv), dim3(32 * p.G), 0, s, 0, p, a, plan);
 }
 
 }  // namespace
 
-cudaError_t launch_attend(const Params& p, const AttendArgs& a, cudaStream_t s) {
-  const dim3 grid(a.q_begin ? a.rows : a.n_members, p.Hkv), block(32 * p.G);
-  return p.d == 128 ? launch_kernel(attend_rows_kernel<128>, grid, block, 0, s, 0, p, a)
-                    : launch_kernel(attend_rows_kernel<64>, grid, block, 0, s, 0, p, a);
+size_t attend_tiles(int B, int max_rows, int G) {
+  const size_t packed = static_cast<size_t>(max_rows / (2 * sub_tokens(G))) + B, grouped = 2 * static_cast<size_t>(B);
+  return packed > grouped ? packed : grouped;
+}
+
+size_t attend_work_bytes(int B, int Hq, int G, int d, int max_rows) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t tiles = attend_tiles(B, max_rows, G);
+  return up(sizeof(PlanHead)) + up(sizeof(Start) * kMaxAttendCtas) + up(8 * (tiles + 1)) + up(sizeof(Tile) * tiles) +
+         up(4 * static_cast<size_t>(B)) +
+         up((2ull * kMaxAttendCtas * 256 + 2ull * B * Hq) * (d + 4) * sizeof(float));
+}
+
+cudaError_t launch_attend(const Params& p, const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          int sms, cudaStream_t s) {
+  if (p.d == 128)
+    return p.bs == 128 ? launch_attend_t<128, 128>(p, a, kmap, vmap, sms, s)
+                       : launch_attend_t<128, 64>(p, a, kmap, vmap, sms, s);
+  return p.bs == 128 ? launch_attend_t<64, 128>(p, a, kmap, vmap, sms, s)
+                     : launch_attend_t<64, 64>(p, a, kmap, vmap, sms, s);
 }
 
 }  // namespace prr

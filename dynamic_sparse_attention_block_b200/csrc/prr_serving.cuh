@@ -10,6 +10,7 @@ namespace prr {
 struct ServeLayout {
   size_t status;   // int32 status word
   size_t pages;    // page bookkeeping, int32 words (see pages.cu)
+  size_t attend;   // plan and partials of the attention calls (see attend.cu)
   size_t total;
 };
 
@@ -47,7 +48,11 @@ struct AttendArgs {
   int n_members, n_groups;
   uint16_t* out;
   float* lse;
+  void* work;    // the workspace's part for these calls, laid out for max_rows packed rows
+  int max_rows;
 };
+
+constexpr int kMaxAttendCtas = 160;  // the workspace holds partials for so many
 
 struct PageArgs {
   uint16_t* kc;
@@ -66,9 +71,12 @@ struct PageArgs {
 };
 
 size_t page_work_words(const Params& p);
+size_t attend_tiles(int B, int max_rows, int G);
+size_t attend_work_bytes(int B, int Hq, int G, int d, int max_rows);
 
 cudaError_t launch_append_prompt(const Params& p, const AppendArgs& a, cudaStream_t s);
-cudaError_t launch_attend(const Params& p, const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend(const Params& p, const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          int sms, cudaStream_t s);
 cudaError_t launch_cache_reserve(const Params& p, const PageArgs& a, const int* want, cudaStream_t s);
 cudaError_t launch_cache_fork(const Params& p, const PageArgs& a, const int* parents, const int* children, int n,
                               cudaStream_t s);

@@ -13,8 +13,9 @@ ServeLayout serve_layout(const prr_dims* d, int32_t max_rows) {
   size_t off = 256;  // status word
   L.pages = off;
   off = align256(off + 4 * page_work_words(p));
+  L.attend = off;
+  off = align256(off + attend_work_bytes(d->B, d->Hq, d->Hq / d->Hkv, d->d, max_rows));
   L.total = off;
-  (void)max_rows;
   return L;
 }
 
@@ -22,6 +23,16 @@ bool rows_ok(int32_t rows) { return rows >= 0 && rows <= (1 << 30); }
 
 // Distance of two packed rows of `heads` heads.
 bool stride_ok(int64_t stride, int64_t heads, int64_t d) { return stride >= heads * d && stride % 8 == 0; }
+
+// Tensor maps of the caches and the launch, for both attention calls.
+prr_status attend(const prr_dims* d, Params& p, AttendArgs& a, void* ws, const ServeLayout& L, int32_t max_rows,
+                  cudaStream_t stream) {
+  a.work = static_cast<unsigned char*>(ws) + L.attend;
+  a.max_rows = max_rows;
+  CUtensorMap km, vm;
+  if (!make_kv_map(&km, p.kc, d) || !make_kv_map(&vm, p.vc, d)) return PRR_ERR_CUDA;
+  return cuda_status(launch_attend(p, a, km, vm, device_info().sms, stream));
+}
 
 Params serve_params(const prr_dims* d, void* ws, const ServeLayout& L) {
   Params p = base_params(d, nullptr, true);
@@ -100,7 +111,7 @@ prr_status prr_attend_prompt(const prr_dims* dims, const uint16_t* q, int64_t q_
   a.rows = rows;
   a.out = out;
   a.lse = lse;
-  return cuda_status(launch_attend(p, a, stream));
+  return attend(dims, p, a, ws, L, rows, stream);
 }
 
 prr_status prr_attend_shared(const prr_dims* dims, const uint16_t* q, int64_t q_stride, const int32_t* members,
@@ -130,7 +141,7 @@ prr_status prr_attend_shared(const prr_dims* dims, const uint16_t* q, int64_t q_
   a.n_groups = n_groups;
   a.out = out;
   a.lse = lse;
-  return cuda_status(launch_attend(p, a, stream));
+  return attend(dims, p, a, ws, L, 1, stream);
 }
 
 prr_status prr_cache_reserve(const prr_dims* dims, const int32_t* want_lens, const prr_cache_buffers* cache, void* ws,
