@@ -15,8 +15,9 @@
 // tile of a batch in groups) leaves fp32 partials (m, sum, O) that combine kernels merge.
 //
 // A CTA (one per SM) runs, per tile piece: one thread that issues the TMA copies of K and
-// V blocks through a ring of stages; one that issues the products; and two groups of 128
-// threads, one per 128 rows, each thread owning one row.  For rows t in {0, 1}:
+// V blocks through a ring of stages; one that issues the products; two warps that bring
+// the next piece's rows of Q as soon as the last product has read the present ones; and two groups of
+// 128 threads, one per 128 rows, each thread owning one row.  For rows t in {0, 1}:
 //   S_t = Q_t K^T (tensor memory), softmax group t turns S_t into P_t = 2^(s' - m) in place,
 //   O_t += P_t V (tensor memory), with S of one half and the softmax of the other overlapping.
 // P is rounded to bf16 (the product's operand type): half a step, 2^-8 of each weight at most; its sum,
@@ -32,7 +33,7 @@ namespace {
 constexpr int kBlock = 128;         // tokens per step
 constexpr float kGrow = 8.0f;       // log2 of the growth that moves the reference m
 constexpr int kPlanThreads = 1024;
-constexpr int kAttendThreads = 320;  // 2 x 128 softmax threads, a product warp, a copy warp
+constexpr int kAttendThreads = 384;  // 2 x 128 softmax threads; warps for products, copies, Q (2)
 constexpr int kCombineRows = 64;
 
 __host__ __device__ constexpr int sub_tokens(int G) { return kBlock / G; }  // packed tokens per 128 rows
@@ -258,26 +259,29 @@ struct Piece {
 };
 
 struct Walk {
-  const Plan* plan;
+  const Tile* tiles;
   long long left;
-  int head, tile, off;
+  int count, head, tile, off;
+  Tile ahead;  // tile `tile`, on its way before it is needed
 
-  __device__ Walk(const Plan& pl, int kv_heads, int c) : plan(&pl) {
-    const PlanHead h = *pl.head;
+  __device__ Walk(const Plan& plan, int kv_heads, int c) : tiles(plan.tile) {
+    const PlanHead h = *plan.head;
+    count = h.tiles;
     left = 0;
     if (c < h.ctas) {
       const long long units = h.per_head * kv_heads;
       left = first_unit(units, h.ctas, c + 1) - first_unit(units, h.ctas, c);
-      const Start s = pl.start[c];
+      const Start s = plan.start[c];
       head = s.head;
       tile = s.tile;
       off = s.off;
+      ahead = tiles[tile];
     }
   }
 
-  __device__ bool next(Piece* x) {
+  __device__ __forceinline__ bool next(Piece* x) {
     while (left > 0) {
-      x->t = plan->tile[tile];
+      x->t = ahead;
       const int take = static_cast<int>(min(left, static_cast<long long>(x->t.blocks - off)));
       x->head = head;
       x->b0 = off;
@@ -286,10 +290,11 @@ struct Walk {
       x->whole = take == x->t.blocks;
       left -= take;
       off = 0;
-      if (++tile == plan->head->tiles) {
+      if (++tile == count) {
         tile = 0;
         ++head;
       }
+      ahead = tiles[tile];
       if (take > 0) return true;
     }
     return false;
@@ -306,16 +311,16 @@ struct Smem {
   static constexpr int Q = 0;
   static constexpr int KV = 2 * TILE;
   static constexpr int BARS = KV + STAGES * TILE;
-  static constexpr int BYTES = BARS + 256;
+  static constexpr int BYTES = BARS + 384;
 };
 
 struct Bars {
   uint64_t full[10], empty[10];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain;
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_free[2], drain;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 256, "barriers fit behind the stages");
+static_assert(sizeof(Bars) <= 384, "barriers fit behind the stages");
 
 // Bounded wait of the kernel's roles, by whole warps; one that gives up makes all give up.
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t phase, volatile int* abort, int* status) {
@@ -354,7 +359,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(&bars.empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars.q_full[t], 128);
+      mbar_init(&bars.q_full[t], 32);
+      mbar_init(&bars.q_free[t], 1);
       mbar_init(&bars.s_full[t], 1);
       mbar_init(&bars.p_full[t], 128);
       mbar_init(&bars.o_full[t], 1);
@@ -440,8 +446,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         mbar_wait(&bars.full[f % NS], static_cast<uint32_t>(f / NS) & 1, p.status);
   } else if (warp == 8) {
     // ---------------------------------------------------------------- products
-    constexpr uint32_t QK = mma_desc(128, 128, false), PV = mma_desc(128, D, true);
-    const uint32_t sQ = smem_addr(smem + L::Q), sKV = smem_addr(smem + L::KV);
+    // a negative scale negates Q, so that the largest product has the largest logit
+    const uint32_t QK = mma_desc(128, 128, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
+    constexpr uint32_t PV = mma_desc(128, D, true);
+    const uint64_t dQ = tile_desc(smem_addr(smem + L::Q), 16, 1024);
+    const uint64_t dK = tile_desc(smem_addr(smem + L::KV), 16, 1024), dV = tile_desc(smem_addr(smem + L::KV), L::SLAB, 1024);
     uint32_t qph = 0, pph = 0, oph = 0;  // phases, bit t for rows t
     int s = 0;
     uint32_t ph = 0;
@@ -449,10 +458,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     auto qk = [&](int t, int stage) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k / 4) * L::SLAB + (k % 4) * 32;
-        mma_ss(tmem + S_COL + t * 128, tile_desc(sQ + t * L::TILE + at, 16, 1024),
-               tile_desc(sKV + stage * L::TILE + at, 16, 1024), QK, k > 0);
+        const uint32_t at = ((k / 4) * L::SLAB + (k % 4) * 32) >> 4;
+        mma_ss(tmem + S_COL + t * 128, dQ + (t * (L::TILE >> 4) + at), dK + (stage * (L::TILE >> 4) + at), QK, k > 0);
       }
+    };
+    auto pv = [&](int t, int stage, bool add) {
+#pragma unroll
+      for (int k = 0; k < kBlock / 16; ++k)
+        mma_ts(tmem + O_COL + t * D, tmem + S_COL + t * 128 + k * 8, dV + (stage * (L::TILE >> 4) + k * 128), PV,
+               add || k > 0);
     };
     while (ok && walk.next(&x)) {
       const int halves = x.t.ntok > tps ? 2 : 1;
@@ -463,13 +477,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       ok = ok && role_wait(&bars.full[s], ph, abort, p.status);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
-        for (int t = 0; t < halves; ++t) {
-          qk(t, s);
-          tc_commit(&bars.s_full[t]);
-        }
+      const bool one = x.b1 - x.b0 == 1;
+      if (elect_one()) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t < halves) {
+            qk(t, s);
+            tc_commit(&bars.s_full[t]);
+            if (one) tc_commit(&bars.q_free[t]);
+          }
         tc_commit(&bars.empty[s]);
       }
+      __syncwarp();
       if (++s == NS) {
         s = 0;
         ph ^= 1;
@@ -482,7 +501,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           ph ^= 1;
         }
         const bool more = b + 1 < x.b1;
-        for (int t = 0; ok && t < halves; ++t) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || t >= halves) break;
           if (t == 0) {
             ok = role_wait(&bars.full[vs], vph, abort, p.status);
             const int valid = x.t.kv1 - (x.t.kv0 + b * kBlock);
@@ -504,24 +525,23 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           if (ok && more && t == 0) ok = role_wait(&bars.full[s], ph, abort, p.status);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-              mma_ts(tmem + O_COL + t * D, tmem + S_COL + t * 128 + k * 8,
-                     tile_desc(sKV + vs * L::TILE + k * 2048, L::SLAB, 1024), PV, b > x.b0 || k > 0);
+          if (elect_one()) {
+            pv(t, vs, b > x.b0);
             if (more) {
               qk(t, s);
               tc_commit(&bars.s_full[t]);
+              if (b + 2 == x.b1) tc_commit(&bars.q_free[t]);
             } else {
               tc_commit(&bars.o_full[t]);
             }
+            if (t == halves - 1) {
+              tc_commit(&bars.empty[vs]);
+              if (more) tc_commit(&bars.empty[s]);
+            }
           }
+          __syncwarp();
         }
         if (!ok) break;
-        if (lane == 0) {
-          tc_commit(&bars.empty[vs]);
-          if (more) tc_commit(&bars.empty[s]);
-        }
         if (more && ++s == NS) {
           s = 0;
           ph ^= 1;
@@ -529,9 +549,46 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       }
     }
     __syncwarp();
-    if (*abort && lane == 0) {  // products still in flight end before their memory is given back
-      tc_commit(&bars.drain);
+    if (__any_sync(0xFFFFFFFFu, *abort)) {  // products still in flight end before their memory is given back
+      if (elect_one()) tc_commit(&bars.drain);
       mbar_wait(&bars.drain, 0, p.status);
+      __syncwarp();
+    }
+  } else if (warp >= 10) {
+    // ---------------------------------------------------------------- rows of Q, half t
+    const int t = warp - 10;
+    uint32_t fph = 1;
+    bool ok = true;
+    while (ok && walk.next(&x)) {
+      const int ntok = min(tps, x.t.ntok - t * tps);
+      if (ntok <= 0) continue;
+      ok = role_wait(&bars.q_free[t], fph, abort, p.status);
+      fph ^= 1;
+      if (!ok) break;
+      // 16-byte chunk c of row r, swizzled as the products read it; rows of no one keep what is there,
+      // which reaches no other row's result
+      constexpr int C = D / 8, STEP = 32 / C;
+      const int c = lane % C;
+      const uint16_t* q = a.q + static_cast<size_t>(x.head) * G * D + c * 8;
+      const uint32_t dst = smem_addr(smem + L::Q + t * L::TILE + (c >> 3) * L::SLAB);
+      int tok = (lane / C) / G, g = (lane / C) % G;
+      const int rows = ntok * G;
+#pragma unroll 4
+      for (int r = lane / C; r < rows; r += STEP) {
+        const int e = x.t.row0 + t * tps + tok;
+        const int row = a.q_begin ? e : plan.row[e];
+        if (row >= 0)
+          cp_async_16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                      q + static_cast<size_t>(row) * a.q_stride + static_cast<size_t>(g) * D);
+        g += STEP;
+        while (g >= G) {
+          g -= G;
+          ++tok;
+        }
+      }
+      cp_async_wait_all();
+      fence_proxy_async();
+      mbar_arrive(&bars.q_full[t]);
     }
     __syncwarp();
   } else {
@@ -540,34 +597,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + S_COL + t * 128 + lanes, tO = tmem + O_COL + t * D + lanes;
     uint32_t sph = 0, oph = 0;
-    // a negative scale changes q's signs, so that the largest product has the largest logit; scale 0 is q = 0
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
-    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    const int tok = tid / G, g = tid - tok * G;
+    // scale 0: every logit 0, and a masked one still -infinity
+    const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     bool ok = true;
     while (ok && walk.next(&x)) {
       const int ntok = min(tps, x.t.ntok - t * tps);
       if (ntok <= 0) continue;
-      // rows of Q, swizzled as the products read them
-      for (int i = tid; i < kBlock * (D / 8); i += 128) {
-        const int r = i / (D / 8), c = i % (D / 8), tok = r / G;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (tok < ntok) {
-          const int e = x.t.row0 + t * tps + tok;
-          const int row = a.q_begin ? e : plan.row[e];
-          if (row >= 0)
-            w = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(row) * a.q_stride +
-                                                     static_cast<size_t>(x.head * G + r % G) * D + c * 8));
-          w.x = (w.x ^ flip) & keep;
-          w.y = (w.y ^ flip) & keep;
-          w.z = (w.z ^ flip) & keep;
-          w.w = (w.w ^ flip) & keep;
-        }
-        *reinterpret_cast<uint4*>(smem + L::Q + t * L::TILE + (c >> 3) * L::SLAB + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
-      }
-      fence_proxy_async();
-      mbar_arrive(&bars.q_full[t]);
-
-      const int tok = tid / G;
       const bool mine = tok < ntok;
       const bool work = __any_sync(0xFFFFFFFFu, mine);
       const int e = x.t.row0 + t * tps + (mine ? tok : 0);
@@ -581,7 +617,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (work) {
-          uint32_t s[kBlock];
+          float s[kBlock];
 #pragma unroll
           for (int c = 0; c < kBlock; c += 32) tmem_ld32(tS + c, s + c);
           tmem_wait_ld();
@@ -589,40 +625,49 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           if (__any_sync(0xFFFFFFFFu, lim < kBlock)) {
 #pragma unroll
             for (int c = 0; c < kBlock; ++c)
-              if (c >= lim) s[c] = 0xFF800000u;
+              if (c >= lim) s[c] = -INFINITY;
           }
-          float mx = -INFINITY;
+          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 0; c < kBlock; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
-          const float m1 = fmaxf(m, mx * scale);
+          for (int c = 4; c < kBlock; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mx[i] = c + 4 + i < kBlock ? fmaxf(fmaxf(mx[i], s[c + i]), s[c + 4 + i]) : fmaxf(mx[i], s[c + i]);
+          const float m1 = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
           if (b == x.b0) {
             m = m1;
           } else if (__any_sync(0xFFFFFFFFu, m1 - m > kGrow || (m == -INFINITY && m1 > m))) {
             const float f = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
             m = m1;
             sum *= f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
+              float o[32];
               tmem_ld32(tO + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              for (int i = 0; i < 32; ++i) o[i] *= f;
               tmem_st32(tO + c, o);
             }
           }
+          const float2 sc = make_float2(scale, scale);
           const float base = m == -INFINITY ? 0.f : m;
-          float part = 0.f;
+          const float2 off = make_float2(-base, -base);
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < kBlock; c += 2) {
-            const float w0 = exp2_fast(fmaf(__uint_as_float(s[c]), scale, -base));
-            const float w1 = exp2_fast(fmaf(__uint_as_float(s[c + 1]), scale, -base));
-            part += w0 + w1;
-            s[c / 2] = pack_bf16(w0, w1);
+          for (int h = 0; h < 4; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float2 y = fma2(make_float2(s[h * 32 + 2 * c], s[h * 32 + 2 * c + 1]), sc, off);
+              y.x = exp2_fast(y.x);
+              y.y = exp2_fast(y.y);
+              part[c & 1] = add2(part[c & 1], y);
+              w[c] = pack_bf16(y.x, y.y);
+            }
+            tmem_st16(tS + h * 16, w);
           }
-          sum += part;
-          tmem_st32(tS, s);
-          tmem_st32(tS + 32, s + 32);
+          sum += (part[0].x + part[1].x) + (part[0].y + part[1].y);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -633,7 +678,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (work) {
-        const int hq = x.head * G + tid % G;
+        const int hq = x.head * G + g;
         const bool direct = a.q_begin && x.whole;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const size_t at = static_cast<size_t>(row < 0 ? 0 : row) * p.Hq + hq;
@@ -651,23 +696,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
+          float o[32];
           tmem_ld32(tO + c, o);
           tmem_wait_ld();
           if (row >= 0 && direct) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-              w.y = pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-              w.z = pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-              w.w = pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-              *reinterpret_cast<uint4*>(a.out + at * D + c + i) = w;
-            }
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(a.out + at * D + c + i) =
+                  make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                             pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
           } else if (row >= 0) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + 4 + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              *reinterpret_cast<float4*>(part + 4 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
       }
