@@ -30,11 +30,11 @@ namespace prr {
 
 namespace {
 
-constexpr int kBlock = 128;         // tokens per step
+constexpr int kBlock = 128;         // tokens per unit of work
+constexpr int kStep = 64;           // tokens per product: two steps of S in tensor memory, one ahead
 constexpr float kGrow = 8.0f;       // log2 of the growth that moves the reference m
 constexpr int kPlanThreads = 1024;
 constexpr int kAttendThreads = 384;  // 2 x 128 softmax threads; warps for products, copies, Q (2)
-constexpr int kCombineRows = 64;
 
 __host__ __device__ constexpr int sub_tokens(int G) { return kBlock / G; }  // packed tokens per 128 rows
 
@@ -256,6 +256,10 @@ struct Piece {
   int b0, b1;   // blocks of the tile
   bool whole;   // this CTA has all of the tile
   bool first;   // ... has its first block
+
+  __device__ __forceinline__ int steps() const {  // of kStep tokens
+    return (min(t.kv1 - t.kv0, b1 * kBlock) - b0 * kBlock + kStep - 1) / kStep;
+  }
 };
 
 struct Walk {
@@ -305,22 +309,25 @@ struct Walk {
 
 template <int D>
 struct Smem {
-  static constexpr int TILE = kBlock * D * 2;  // one Q, K or V tile
-  static constexpr int SLAB = kBlock * 128;    // one 64-channel slab of it
-  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int Q_TILE = 128 * D * 2;      // 128 rows of Q
+  static constexpr int Q_SLAB = 128 * 128;        // 64 channels of them
+  static constexpr int TILE = kStep * D * 2;      // K or V of one step
+  static constexpr int SLAB = kStep * 128;
+  static constexpr int STAGES = D == 128 ? 10 : 20;
   static constexpr int Q = 0;
-  static constexpr int KV = 2 * TILE;
+  static constexpr int KV = 2 * Q_TILE;
   static constexpr int BARS = KV + STAGES * TILE;
-  static constexpr int BYTES = BARS + 384;
+  static constexpr int BYTES = BARS + 768;
 };
 
 struct Bars {
-  uint64_t full[10], empty[10];
-  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_free[2], drain;
+  uint64_t full[20], empty[20], clean[20];  // of the stages; clean: rows of V past the last token are zero
+  uint64_t s_full[2][2], p_full[2][2];  // [rows t][buffer]
+  uint64_t q_full[2], q_free[2], o_step[2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 384, "barriers fit behind the stages");
+static_assert(sizeof(Bars) <= 768, "barriers fit behind the stages");
 
 // Bounded wait of the kernel's roles, by whole warps; one that gives up makes all give up.
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t phase, volatile int* abort, int* status) {
@@ -338,13 +345,45 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t phase, volatil
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-template <int D, int BS>
+// The same for a single thread.
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t phase, volatile int* abort, int* status) {
+  if (mbar_try_wait(bar, phase)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, phase)) {
+    if (*abort) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      report(status, kDevWaitTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+// A position in the ring of stages.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void skip(int n) {
+    ph ^= static_cast<uint32_t>((s + n) / N) & 1;
+    s = (s + n) % N;
+  }
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D>
 __global__ void __launch_bounds__(kAttendThreads, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const __grid_constant__ Params p, const __grid_constant__ AttendArgs a,
-                  const __grid_constant__ Plan plan) {
+    attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p,
+                  const __grid_constant__ AttendArgs a, const __grid_constant__ Plan plan) {
   using L = Smem<D>;
-  constexpr int NS = L::STAGES, NREG = D / 64, HALVES = kBlock / BS;
+  constexpr int NS = L::STAGES, NREG = D / 64;
   constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -356,17 +395,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 1);
+      mbar_init(&bars.empty[i], 2);  // both halves have used it
+      mbar_init(&bars.clean[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars.q_full[t], 32);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.s_full[t][i], 1);
+        mbar_init(&bars.p_full[t][i], 4);
+      }
+      mbar_init(&bars.q_full[t], a.q_begin ? 1 : 32);
       mbar_init(&bars.q_free[t], 1);
-      mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.o_step[t], 1);
       mbar_init(&bars.o_full[t], 1);
-      mbar_init(&bars.o_free[t], 128);
+      mbar_init(&bars.o_free[t], 4);
+      mbar_init(&bars.drain[t], 1);
     }
-    mbar_init(&bars.drain, 1);
     bars.abort = 0;
     fence_barrier_init();
     prefetch_tensormap(&kmap);
@@ -382,261 +425,271 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   volatile int* abort = &bars.abort;
   Walk walk(plan, p.Hkv, blockIdx.x);
   Piece x;
+  bool ok = true;
 
-  if (warp == 9) {
-    // ---------------------------------------------------------------- copies
-    int s = 0;
-    uint32_t ph = 0;      // phase of the ring: stage s has been filled ph times (mod 2)
-    long long fills = 0;  // copies issued, in stages
-    bool ok = true;
+  if (warp == 10) {
+    // ---------------------------------------------------------------- copies: K0 K1 V0 K2 V1 K3 ...
+    Ring<NS> ring;
+    long long fills = 0;
     while (ok && walk.next(&x)) {
-      int page = 0, have = -1;  // lane i: the page of cache block have + i
-      for (int b = x.b0; ok && b < x.b1; ++b) {
-        const int t0 = x.t.kv0 + b * kBlock;
-        int slice[2], tok[2], n = 0;
-#pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf) {
-          const int th = t0 + hf * BS;
-          if (th < x.t.kv1) {
-            n = hf + 1;
-            if (p.table) {
-              const int blk = th / BS;
-              if (have < 0 || blk >= have + 32) {
-                have = blk;
-                page = blk + lane < (x.t.kv1 + BS - 1) / BS
+      const int begin = x.t.kv0 + x.b0 * kBlock, n = x.steps();
+      int page[2] = {0, 0}, have[2] = {-1, -1};  // lane i: the page of cache block have + i; for K, for V
+      for (int i = 0; ok && i < 2 * n; ++i) {
+        const int kv = i == 0 || (i & 1 && i < 2 * n - 1) ? 0 : 1;  // one step of K ahead of V
+        const int j = kv ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2;
+        const int tok0 = begin + j * kStep;
+        int row = tok0, slice = x.t.seq * p.Hkv + x.head;
+        if (p.table) {
+          const int blk = tok0 / p.bs;
+          if (have[kv] < 0 || blk >= have[kv] + 32) {
+            have[kv] = blk;
+            page[kv] = blk + lane < (x.t.kv1 + p.bs - 1) / p.bs
                            ? p.table[static_cast<size_t>(x.t.seq) * p.maxnb + blk + lane] : 0;
-              }
-              const int pg = __shfl_sync(0xFFFFFFFFu, page, blk - have);
-              const bool good = pg >= 0 && pg < p.pages;
-              if (!good && lane == 0) report(p.status, kDevBadRange);
-              slice[hf] = good ? pg * p.Hkv + x.head : p.pages * p.Hkv;  // past the map: zeros
-              tok[hf] = 0;
-            } else {
-              slice[hf] = x.t.seq * p.Hkv + x.head;
-              tok[hf] = th;
-            }
           }
+          const int pg = __shfl_sync(0xFFFFFFFFu, page[kv], blk - have[kv]);
+          const bool good = pg >= 0 && pg < p.pages;
+          if (!good && lane == 0) report(p.status, kDevBadRange);
+          slice = good ? pg * p.Hkv + x.head : p.pages * p.Hkv;  // past the map: zeros
+          row = tok0 - blk * p.bs;
         }
+        ok = role_wait(&bars.empty[ring.s], ring.ph ^ 1, abort, p.status);
+        if (!ok) break;
+        if (lane == 0) {
+          unsigned char* dst = smem + L::KV + ring.s * L::TILE;
+          mbar_expect_tx(&bars.full[ring.s], L::TILE);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && role_wait(&bars.empty[s], ph ^ 1, abort, p.status);
-          if (ok && lane == 0) {
-            unsigned char* dst = smem + L::KV + s * L::TILE;
-            mbar_expect_tx(&bars.full[s], n * BS * D * 2);
-#pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf)
-              if (hf < n)
-#pragma unroll
-                for (int r = 0; r < NREG; ++r)
-                  tma_load_3d(dst + r * L::SLAB + hf * BS * 128, kv ? &vmap : &kmap, &bars.full[s], r * 64, tok[hf],
-                              slice[hf]);
-          }
-          if (ok) ++fills;
-          if (ok && ++s == NS) {
-            s = 0;
-            ph ^= 1;
-          }
+          for (int r = 0; r < NREG; ++r)
+            tma_load_3d(dst + r * L::SLAB, kv ? &vmap : &kmap, &bars.full[ring.s], r * 64, row, slice);
         }
+        __syncwarp();
+        ++fills;
+        ring.next();
       }
     }
-    __syncwarp();
     // copies still in flight land before the CTA ends (all have, unless a wait ran out)
     if (*abort && lane == 0)
       for (long long f = max(0ll, fills - NS); f < fills; ++f)
         mbar_wait(&bars.full[f % NS], static_cast<uint32_t>(f / NS) & 1, p.status);
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- products
+  } else if (warp >= 8 && warp < 10) {
+    // ---------------------------------------------------------------- products of rows t, by one thread
+    const int t = warp - 8;
     // a negative scale negates Q, so that the largest product has the largest logit
-    const uint32_t QK = mma_desc(128, 128, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
+    const uint32_t QK = mma_desc(128, kStep, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t PV = mma_desc(128, D, true);
     const uint64_t dQ = tile_desc(smem_addr(smem + L::Q), 16, 1024);
     const uint64_t dK = tile_desc(smem_addr(smem + L::KV), 16, 1024), dV = tile_desc(smem_addr(smem + L::KV), L::SLAB, 1024);
-    uint32_t qph = 0, pph = 0, oph = 0;  // phases, bit t for rows t
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    auto qk = [&](int t, int stage) {
+    uint32_t qph = 0, fph = 1, cph = 0;  // phases: Q full, O free; V clean, a bit for each stage
+    uint32_t asked = 0, used = 0;         // steps whose S has been asked for, whose P has been used
+    Ring<NS> ring;
+    // (descriptors differ in their low words, by address / 16: no more than an addition for each product)
+    auto qk = [&](int stage, uint32_t buf) {
+      const uint64_t q = dQ + t * (L::Q_TILE >> 4), k0 = dK + static_cast<uint32_t>(stage) * (L::TILE >> 4);
+      const uint32_t d = tmem + S_COL + t * 128 + buf * 64;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = ((k / 4) * L::SLAB + (k % 4) * 32) >> 4;
-        mma_ss(tmem + S_COL + t * 128, dQ + (t * (L::TILE >> 4) + at), dK + (stage * (L::TILE >> 4) + at), QK, k > 0);
-      }
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(d, q + ((k / 4) * (L::Q_SLAB >> 4) + (k % 4) * 2), k0 + ((k / 4) * (L::SLAB >> 4) + (k % 4) * 2), QK, k > 0);
     };
-    auto pv = [&](int t, int stage, bool add) {
+    auto pv = [&](int stage, uint32_t buf, bool add) {
+      const uint64_t v0 = dV + static_cast<uint32_t>(stage) * (L::TILE >> 4);
+      const uint32_t d = tmem + O_COL + t * D, pt = tmem + S_COL + t * 128 + buf * 64;
 #pragma unroll
-      for (int k = 0; k < kBlock / 16; ++k)
-        mma_ts(tmem + O_COL + t * D, tmem + S_COL + t * 128 + k * 8, dV + (stage * (L::TILE >> 4) + k * 128), PV,
-               add || k > 0);
+      for (int k = 0; k < kStep / 16; ++k) mma_ts(d, pt + k * 8, v0 + k * 128, PV, add || k > 0);
     };
-    while (ok && walk.next(&x)) {
-      const int halves = x.t.ntok > tps ? 2 : 1;
-      for (int t = 0; ok && t < halves; ++t) {
-        ok = role_wait(&bars.q_full[t], (qph >> t) & 1, abort, p.status);
-        qph ^= 1u << t;
-      }
-      ok = ok && role_wait(&bars.full[s], ph, abort, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      const bool one = x.b1 - x.b0 == 1;
-      if (elect_one()) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (t < halves) {
-            qk(t, s);
-            tc_commit(&bars.s_full[t]);
-            if (one) tc_commit(&bars.q_free[t]);
+    if (elect_one()) {
+      while (ok && walk.next(&x)) {
+        const int halves = x.t.ntok > tps ? 2 : 1, n = x.steps();
+        const bool tail = (x.t.kv1 - x.t.kv0 - x.b0 * kBlock) - (n - 1) * kStep < kStep;
+        if (t >= halves) {  // nothing here: let the stages pass
+          for (int i = 0; ok && i < 2 * n; ++i, ring.next()) {
+            ok = thread_wait(&bars.full[ring.s], ring.ph, abort, p.status);
+            if (ok) mbar_arrive(&bars.empty[ring.s]);
+            if (tail && i == 2 * n - 1) cph ^= 1u << ring.s;
           }
-        tc_commit(&bars.empty[s]);
-      }
-      __syncwarp();
-      if (++s == NS) {
-        s = 0;
-        ph ^= 1;
-      }
-      for (int b = x.b0; ok && b < x.b1; ++b) {
-        const int vs = s;
-        const uint32_t vph = ph;
-        if (++s == NS) {
-          s = 0;
-          ph ^= 1;
+          continue;
         }
-        const bool more = b + 1 < x.b1;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || t >= halves) break;
-          if (t == 0) {
-            ok = role_wait(&bars.full[vs], vph, abort, p.status);
-            const int valid = x.t.kv1 - (x.t.kv0 + b * kBlock);
-            if (ok && valid < kBlock) {  // rows past the last token may hold anything: 0 * NaN is not 0
-              for (int i = valid * 8 + lane; i < kBlock * 8; i += 32)
-#pragma unroll
-                for (int r = 0; r < NREG; ++r)
-                  *reinterpret_cast<uint4*>(smem + L::KV + vs * L::TILE + r * L::SLAB + i * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async();
-              __syncwarp();
-            }
-          }
-          ok = ok && role_wait(&bars.p_full[t], (pph >> t) & 1, abort, p.status);
-          pph ^= 1u << t;
-          if (ok && b == x.b0) {  // the previous piece's O has been read
-            ok = role_wait(&bars.o_free[t], ((oph >> t) & 1) ^ 1, abort, p.status);
-            oph ^= 1u << t;
-          }
-          if (ok && more && t == 0) ok = role_wait(&bars.full[s], ph, abort, p.status);
+        ok = thread_wait(&bars.q_full[t], qph, abort, p.status);
+        qph ^= 1;
+        for (int j = 0; ok && j < min(2, n); ++j) {  // S of the first two steps
+          ok = thread_wait(&bars.full[ring.s], ring.ph, abort, p.status);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
-            pv(t, vs, b > x.b0);
-            if (more) {
-              qk(t, s);
-              tc_commit(&bars.s_full[t]);
-              if (b + 2 == x.b1) tc_commit(&bars.q_free[t]);
-            } else {
-              tc_commit(&bars.o_full[t]);
-            }
-            if (t == halves - 1) {
-              tc_commit(&bars.empty[vs]);
-              if (more) tc_commit(&bars.empty[s]);
-            }
+          qk(ring.s, asked & 1);
+          tc_commit(&bars.s_full[t][asked & 1]);
+          if (j == n - 1) tc_commit(&bars.q_free[t]);
+          tc_commit(&bars.empty[ring.s]);
+          ++asked;
+          ring.next();
+        }
+        // the previous piece's O has been read
+        ok = ok && thread_wait(&bars.o_free[t], fph, abort, p.status);
+        fph ^= 1;
+        for (int j = 0; ok && j < n; ++j) {
+          const bool more = j + 2 < n;
+          const uint32_t buf = used & 1;
+          const Ring<NS> v = ring;
+          ring.next();
+          const Ring<NS> k2 = ring;
+          if (more) ring.next();
+          ok = thread_wait(&bars.full[v.s], v.ph, abort, p.status);
+          if (ok && more) ok = thread_wait(&bars.full[k2.s], k2.ph, abort, p.status);
+          if (ok && j == n - 1 && tail) {
+            ok = thread_wait(&bars.clean[v.s], (cph >> v.s) & 1, abort, p.status);
+            cph ^= 1u << v.s;
+          }
+          ok = ok && thread_wait(&bars.p_full[t][buf], (used >> 1) & 1, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          pv(v.s, buf, j > 0);
+          tc_commit(&bars.o_step[t]);
+          if (more) {
+            qk(k2.s, buf);  // runs behind the product that reads P there
+            tc_commit(&bars.s_full[t][buf]);
+            if (j + 3 == n) tc_commit(&bars.q_free[t]);
+            tc_commit(&bars.empty[k2.s]);
+            ++asked;
+          } else if (j == n - 1) {
+            tc_commit(&bars.o_full[t]);
+          }
+          tc_commit(&bars.empty[v.s]);
+          ++used;
+        }
+      }
+      if (*abort) {  // products still in flight end before their memory is given back
+        tc_commit(&bars.drain[t]);
+        mbar_wait(&bars.drain[t], 0, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- rows of Q; the last rows of V
+    uint32_t fph = 3;  // phases, bit t for rows t
+    Ring<NS> ring;     // the stage behind the piece's last
+    Ring<NS> v;        // the stage of its last V
+    int valid = kStep;
+    // Rows past the last token may hold anything, and 0 * NaN is not 0.  (Called once the piece's last product
+    // with Q is through: the stage's phase is then not ambiguous.)
+    auto clean = [&] {
+      ok = ok && role_wait(&bars.full[v.s], v.ph, abort, p.status);
+      if (!ok) return;
+      for (int i = valid * 8 + lane; i < kStep * 8; i += 32)
+#pragma unroll
+        for (int r = 0; r < NREG; ++r)
+          *reinterpret_cast<uint4*>(smem + L::KV + v.s * L::TILE + r * L::SLAB + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.clean[v.s]);
+    };
+    while (ok && walk.next(&x)) {
+      const int n = x.steps();
+      for (int t = 0; ok && t < 2; ++t) {
+        const int ntok = min(tps, x.t.ntok - t * tps);
+        if (ntok <= 0) break;
+        ok = role_wait(&bars.q_free[t], (fph >> t) & 1, abort, p.status);
+        fph ^= 1u << t;
+        if (ok && t == 0 && valid < kStep) clean();  // of the piece before
+        if (!ok) break;
+        if (a.q_begin) {  // packed rows: G heads of tps tokens are one box (rows behind the tile's reach no other's result)
+          if (lane == 0) {
+            mbar_expect_tx(&bars.q_full[t], NREG * 128 * G * tps);
+#pragma unroll
+            for (int r = 0; r < NREG; ++r)
+              tma_load_3d(smem + L::Q + t * L::Q_TILE + r * L::Q_SLAB, &qmap, &bars.q_full[t], r * 64, x.head * G,
+                          x.t.row0 + t * tps);
           }
           __syncwarp();
+          continue;
         }
-        if (!ok) break;
-        if (more && ++s == NS) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    __syncwarp();
-    if (__any_sync(0xFFFFFFFFu, *abort)) {  // products still in flight end before their memory is given back
-      if (elect_one()) tc_commit(&bars.drain);
-      mbar_wait(&bars.drain, 0, p.status);
-      __syncwarp();
-    }
-  } else if (warp >= 10) {
-    // ---------------------------------------------------------------- rows of Q, half t
-    const int t = warp - 10;
-    uint32_t fph = 1;
-    bool ok = true;
-    while (ok && walk.next(&x)) {
-      const int ntok = min(tps, x.t.ntok - t * tps);
-      if (ntok <= 0) continue;
-      ok = role_wait(&bars.q_free[t], fph, abort, p.status);
-      fph ^= 1;
-      if (!ok) break;
-      // 16-byte chunk c of row r, swizzled as the products read it; rows of no one keep what is there,
-      // which reaches no other row's result
-      constexpr int C = D / 8, STEP = 32 / C;
-      const int c = lane % C;
-      const uint16_t* q = a.q + static_cast<size_t>(x.head) * G * D + c * 8;
-      const uint32_t dst = smem_addr(smem + L::Q + t * L::TILE + (c >> 3) * L::SLAB);
-      int tok = (lane / C) / G, g = (lane / C) % G;
-      const int rows = ntok * G;
+        // 16-byte chunk c of row r, swizzled as the products read it; rows of no one keep what is there,
+        // which reaches no other row's result
+        constexpr int C = D / 8, STEP = 32 / C;
+        const int c = lane % C;
+        const uint16_t* q = a.q + static_cast<size_t>(x.head) * G * D + c * 8;
+        const uint32_t dst = smem_addr(smem + L::Q + t * L::Q_TILE + (c >> 3) * L::Q_SLAB);
+        int tok = (lane / C) / G, g = (lane / C) % G;
+        const int rows = ntok * G;
 #pragma unroll 4
-      for (int r = lane / C; r < rows; r += STEP) {
-        const int e = x.t.row0 + t * tps + tok;
-        const int row = a.q_begin ? e : plan.row[e];
-        if (row >= 0)
-          cp_async_16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                      q + static_cast<size_t>(row) * a.q_stride + static_cast<size_t>(g) * D);
-        g += STEP;
-        while (g >= G) {
-          g -= G;
-          ++tok;
+        for (int r = lane / C; r < rows; r += STEP) {
+          const int row = plan.row[x.t.row0 + t * tps + tok];
+          if (row >= 0)
+            cp_async_16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                        q + static_cast<size_t>(row) * a.q_stride + static_cast<size_t>(g) * D);
+          g += STEP;
+          while (g >= G) {
+            g -= G;
+            ++tok;
+          }
         }
+        cp_async_wait_all();
+        fence_proxy_async();
+        mbar_arrive(&bars.q_full[t]);
+        __syncwarp();
       }
-      cp_async_wait_all();
-      fence_proxy_async();
-      mbar_arrive(&bars.q_full[t]);
+      ring.skip(2 * n - 1);
+      v = ring;
+      ring.next();
+      valid = (x.t.kv1 - x.t.kv0 - x.b0 * kBlock) - (n - 1) * kStep;
+    }
+    if (ok && valid < kStep) {
+      ok = role_wait(&bars.q_free[0], fph & 1, abort, p.status);
+      if (ok) clean();
     }
     __syncwarp();
+    if (*abort && a.q_begin && lane == 0)  // a copy in flight lands
+      for (int t = 0; t < 2; ++t) mbar_wait(&bars.q_full[t], (fph >> t) & 1, p.status);
   } else {
     // ---------------------------------------------------------------- softmax, rows t
     const int t = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + S_COL + t * 128 + lanes, tO = tmem + O_COL + t * D + lanes;
-    uint32_t sph = 0, oph = 0;
     const int tok = tid / G, g = tid - tok * G;
     // scale 0: every logit 0, and a masked one still -infinity
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
-    bool ok = true;
+    const float2 sc = make_float2(scale, scale);
+    uint32_t step = 0, oph = 0;  // steps of these rows, over all pieces
     while (ok && walk.next(&x)) {
-      const int ntok = min(tps, x.t.ntok - t * tps);
+      const int ntok = min(tps, x.t.ntok - t * tps), n = x.steps();
       if (ntok <= 0) continue;
       const bool mine = tok < ntok;
       const bool work = __any_sync(0xFFFFFFFFu, mine);
       const int e = x.t.row0 + t * tps + (mine ? tok : 0);
       const int row = !mine ? -1 : a.q_begin ? e : plan.row[e];
-      // one past the last token this row reads; rows of no one read all
-      const int end = !mine ? kNoMask : x.t.pos0 == kNoMask ? x.t.kv1 : x.t.pos0 + t * tps + tok + 1;
+      // one past the last token this row reads, from the piece's first; rows of no one read all
+      int lim = !mine ? kNoMask : (x.t.pos0 == kNoMask ? x.t.kv1 : x.t.pos0 + t * tps + tok + 1) -
+                                      (x.t.kv0 + x.b0 * kBlock);
       float m = -INFINITY, sum = 0.f;
-      for (int b = x.b0; ok && b < x.b1; ++b) {
-        ok = role_wait(&bars.s_full[t], sph, abort, p.status);
-        sph ^= 1;
+      for (int j = 0; j < n; ++j, lim -= kStep, ++step) {
+        const uint32_t buf = step & 1;
+        ok = role_wait(&bars.s_full[t][buf], (step >> 1) & 1, abort, p.status);
         if (!ok) break;
         tc_fence_after();
         if (work) {
-          float s[kBlock];
+          const uint32_t tB = tS + buf * 64;
+          float s[kStep];
+          tmem_ld32(tB, s);
+          tmem_ld32(tB + 32, s + 32);
+          tmem_wait_ld32(s);
+          tmem_wait_ld32(s + 32);
+          const bool cut = __any_sync(0xFFFFFFFFu, lim < kStep);
+          if (cut) {
 #pragma unroll
-          for (int c = 0; c < kBlock; c += 32) tmem_ld32(tS + c, s + c);
-          tmem_wait_ld();
-          const int lim = end - (x.t.kv0 + b * kBlock);
-          if (__any_sync(0xFFFFFFFFu, lim < kBlock)) {
-#pragma unroll
-            for (int c = 0; c < kBlock; ++c)
+            for (int c = 0; c < kStep; ++c)
               if (c >= lim) s[c] = -INFINITY;
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 4; c < kBlock; c += 8)
+          for (int c = 4; c < kStep - 4; c += 8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mx[i] = c + 4 + i < kBlock ? fmaxf(fmaxf(mx[i], s[c + i]), s[c + 4 + i]) : fmaxf(mx[i], s[c + i]);
-          const float m1 = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
-          if (b == x.b0) {
+            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
+          const float m1 = fmaxf(m, max3(max3(mx[0], mx[1], s[kStep - 4]), max3(mx[2], mx[3], s[kStep - 3]),
+                                         fmaxf(s[kStep - 2], s[kStep - 1])) * scale);
+          if (j == 0) {
             m = m1;
-          } else if (__any_sync(0xFFFFFFFFu, m1 - m > kGrow || (m == -INFINITY && m1 > m))) {
+          } else if (__any_sync(0xFFFFFFFFu, mine && (m1 - m > kGrow || (m == -INFINITY && m1 > m)))) {
+            // O holds the steps before this one once the last product is through.  (S of this
+            // step came behind the product two steps back, so the phase is not ambiguous.)
+            ok = role_wait(&bars.o_step[t], (step - 1) & 1, abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
             const float f = m1 == -INFINITY ? 1.f : exp2_fast(m - m1);
             m = m1;
             sum *= f;
@@ -644,34 +697,36 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             for (int c = 0; c < D; c += 32) {
               float o[32];
               tmem_ld32(tO + c, o);
-              tmem_wait_ld();
+              tmem_wait_ld32(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] *= f;
               tmem_st32(tO + c, o);
             }
           }
-          const float2 sc = make_float2(scale, scale);
           const float base = m == -INFINITY ? 0.f : m;
           const float2 off = make_float2(-base, -base);
           float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < kStep / 32; ++h) {
             uint32_t w[16];
+            float2 y[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) y[c] = fma2(make_float2(s[h * 32 + 2 * c], s[h * 32 + 2 * c + 1]), sc, off);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) y[c] = make_float2(exp2_fast(y[c].x), exp2_fast(y[c].y));
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              float2 y = fma2(make_float2(s[h * 32 + 2 * c], s[h * 32 + 2 * c + 1]), sc, off);
-              y.x = exp2_fast(y.x);
-              y.y = exp2_fast(y.y);
-              part[c & 1] = add2(part[c & 1], y);
-              w[c] = pack_bf16(y.x, y.y);
+              part[c & 1] = add2(part[c & 1], y[c]);
+              w[c] = pack_bf16(y[c].x, y[c].y);
             }
-            tmem_st16(tS + h * 16, w);
+            tmem_st16(tB + h * 16, w);
           }
           sum += (part[0].x + part[1].x) + (part[0].y + part[1].y);
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&bars.p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t][buf]);
       }
       ok = ok && role_wait(&bars.o_full[t], oph, abort, p.status);
       oph ^= 1;
@@ -698,7 +753,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(tO + c, o);
-          tmem_wait_ld();
+          tmem_wait_ld32(o);
           if (row >= 0 && direct) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
@@ -713,7 +768,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&bars.o_free[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.o_free[t]);
     }
   }
   __syncthreads();
@@ -854,22 +910,22 @@ Plan plan_of(const Params& p, const AttendArgs& a) {
   return plan;
 }
 
-template <int D, int BS>
-cudaError_t launch_attend_t(const Params& p, const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                            int sms, cudaStream_t s) {
+template <int D>
+cudaError_t launch_attend_t(const Params& p, const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                            const CUtensorMap& vmap, int sms, cudaStream_t s) {
   const Plan plan = plan_of(p, a);
   const int span = 2 * sub_tokens(p.G);
   const int slots = a.q_begin ? a.rows / span + p.B : 2 * a.n_members;
   const int ctas = sms < kMaxAttendCtas ? sms : kMaxAttendCtas;
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(attend_kernel<D, BS>));
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(attend_kernel<D>));
   if (e == cudaSuccess) e = launch_kernel(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, 0, p, a, plan, slots, ctas);
   if (e == cudaSuccess)
-    e = launch_kernel(attend_kernel<D, BS>, dim3(ctas), dim3(kAttendThreads), Smem<D>::BYTES + 1024, s, 0, kmap, vmap, p,
-                      a, plan);
+    e = launch_kernel(attend_kernel<D>, dim3(ctas), dim3(kAttendThreads), Smem<D>::BYTES + 1024, s, 0, qmap, kmap,
+                      vmap, p, a, plan);
   if (e != cudaSuccess) return e;
   if (a.q_begin) {
     if (ctas == 1) return e;
-    return launch_kernel(combine_tiles_kernel<D>, dim3(ctas - 1, 256 / kCombineRows * 2), dim3(256), 0, s, 0, p, a, plan);
+    return launch_kernel(combine_tiles_kernel<D>, dim3(ctas - 1, 32), dim3(256), 0, s, 0, p, a, plan);
   }
   return launch_kernel(combine_entries_kernel<D>, dim3(a.n_members, p.Hkv), dim3(32 * p.G), 0, s, 0, p, a, plan);
 }
@@ -889,13 +945,10 @@ size_t attend_work_bytes(int B, int Hq, int G, int d, int max_rows) {
          up((2ull * kMaxAttendCtas * 256 + 2ull * B * Hq) * (d + 4) * sizeof(float));
 }
 
-cudaError_t launch_attend(const Params& p, const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          int sms, cudaStream_t s) {
-  if (p.d == 128)
-    return p.bs == 128 ? launch_attend_t<128, 128>(p, a, kmap, vmap, sms, s)
-                       : launch_attend_t<128, 64>(p, a, kmap, vmap, sms, s);
-  return p.bs == 128 ? launch_attend_t<64, 128>(p, a, kmap, vmap, sms, s)
-                     : launch_attend_t<64, 64>(p, a, kmap, vmap, sms, s);
+cudaError_t launch_attend(const Params& p, const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, int sms, cudaStream_t s) {
+  return p.d == 128 ? launch_attend_t<128>(p, a, qmap, kmap, vmap, sms, s)
+                    : launch_attend_t<64>(p, a, qmap, kmap, vmap, sms, s);
 }
 
 }  // namespace prr

@@ -75,8 +75,8 @@ size_t attend_tiles(int B, int max_rows, int G);
 size_t attend_work_bytes(int B, int Hq, int G, int d, int max_rows);
 
 cudaError_t launch_append_prompt(const Params& p, const AppendArgs& a, cudaStream_t s);
-cudaError_t launch_attend(const Params& p, const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          int sms, cudaStream_t s);
+cudaError_t launch_attend(const Params& p, const AttendArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                          const CUtensorMap& vmap, int sms, cudaStream_t s);
 cudaError_t launch_cache_reserve(const Params& p, const PageArgs& a, const int* want, cudaStream_t s);
 cudaError_t launch_cache_fork(const Params& p, const PageArgs& a, const int* parents, const int* children, int n,
                               cudaStream_t s);

@@ -22,7 +22,6 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {  //
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The barrier gets one arrival once all tcgen05 work this thread has issued is done.
@@ -103,6 +102,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// tmem_wait_ld for the 32 floats r of a load: they are read behind it only.
+__device__ __forceinline__ void tmem_wait_ld32(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
+
 // One thread of the warp, the same one each time the whole warp asks.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -136,11 +146,41 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// 2^y for y in [-inf, 128) on the multiply-add units, which the exponential unit leaves idle, two values
+// at a time and in steps, so that callers can interleave several: y = n + f with n the nearest
+// integer, 2^f by the degree-4 polynomial with constant term 1 whose largest relative error on
+// [-1/2, 1/2] is smallest (2.9e-06), n added to the exponent.  Below -125: 2^-125.
+struct Exp2Poly {
+  float2 y, t, p;
+  static constexpr int kSteps = 8;
+  __device__ __forceinline__ void step(int i) {
+    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+    if (i == 0) y = make_float2(fmaxf(y.x, -125.f), fmaxf(y.y, -125.f));
+    if (i == 1) t = add2(y, make_float2(kBig, kBig));
+    if (i == 2) p = add2(t, make_float2(-kBig, -kBig));
+    if (i == 3) y = fma2(p, make_float2(-1.f, -1.f), y);
+    if (i == 4) p = fma2(y, make_float2(0.009582853f, 0.009582853f), make_float2(0.055906426f, 0.055906426f));
+    if (i == 5) p = fma2(p, y, make_float2(0.24024099f, 0.24024099f));
+    if (i == 6) p = fma2(p, y, make_float2(0.6931242f, 0.6931242f));
+    if (i == 7) {
+      p = fma2(p, y, make_float2(1.f, 1.f));
+      y = make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+    }
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t w;

@@ -112,7 +112,10 @@ def _prompt(c, new, q=None, lse=True, stream=None, tail=3, ws=None):
     out = torch.full((q.shape[0], c.Hq, c.d), 7.0, dtype=torch.bfloat16, device=DEV)
     L = torch.full((q.shape[0], c.Hq), 7.0, device=DEV) if lse else None
     ws = c.ws(q.shape[0]) if ws is None else ws
-    prr.prr_attend_prompt(c.dims, q, _i32(qb), c.seq_lens, c.kc, c.vc, out, L, ws, stream)
+    qb_dev = _i32(qb)
+    if stream is not None:  # what the call reads and writes is made on the current stream
+        stream.wait_stream(torch.cuda.current_stream())
+    prr.prr_attend_prompt(c.dims, q, qb_dev, c.seq_lens, c.kc, c.vc, out, L, ws, stream)
     return q, qb, out, L, ws
 
 
@@ -183,7 +186,6 @@ def test_attend_prompt_same_bits_twice_on_a_side_stream_and_in_a_graph():
     q, qb, out, lse, ws = _prompt(c, [650, 3])
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
-    st.wait_stream(torch.cuda.current_stream())
     _, _, out2, lse2, _ = _prompt(c, [650, 3], q=q, stream=st)
     torch.cuda.synchronize()
     assert torch.equal(out[:653], out2[:653]) and torch.equal(lse[:653], lse2[:653])
