@@ -50,8 +50,11 @@ struct Tile {  // 32 bytes
 };
 constexpr int kNoMask = 1 << 30;
 
-struct Start {  // where a CTA's run begins
-  int head, tile, off, pad;
+struct Start {  // a CTA's run: where it begins, how long it is, and its first tile
+  int head, tile, off, count;  // count: tiles of the plan
+  long long left;
+  long long pad;
+  Tile first;
 };
 
 struct PlanHead {
@@ -100,19 +103,22 @@ __device__ T plan_scan(T v, T* total) {  // exclusive prefix sum over the CTA
   return x - v + (w ? warp_sum[w - 1] : 0);
 }
 
+// The plan's small inputs and its prefix sums are searched in shared memory where they fit.
+constexpr int kPlanSeqs = 2048, kPlanSlots = 2048;
+
 // Tile `slot` of packed prompts.  Sequence b owns the slots floor(q_begin[b] / span) + b
 // ...: at least as many as it has tiles, so a slot finds its tile by bisection; slots left over weigh 0.
-__device__ Tile prompt_tile(const Params& p, const AttendArgs& a, int slot, int span) {
+__device__ Tile prompt_tile(const Params& p, const AttendArgs& a, const int* q_begin, int slot, int span) {
   Tile t = {};
   int lo = 0, hi = p.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (max(a.q_begin[mid], 0) / span + mid <= slot) lo = mid;
+    if (max(q_begin[mid], 0) / span + mid <= slot) lo = mid;
     else hi = mid - 1;
   }
-  const int j = slot - (max(a.q_begin[lo], 0) / span + lo);
+  const int j = slot - (max(q_begin[lo], 0) / span + lo);
   int r0, r1;
-  if (!packed_range(a.q_begin, lo, a.rows, &r0, &r1, p.status, true) || j < 0) return t;
+  if (!packed_range(q_begin, lo, a.rows, &r0, &r1, p.status, true) || j < 0) return t;
   if (j >= (r1 - r0 + span - 1) / span) return t;
   const int len = p.seq_lens[lo];
   if (len < 1 || len > p.cap || r1 - r0 > len) {
@@ -176,14 +182,24 @@ __device__ bool group_entry(const Params& p, const AttendArgs& a, int i, Entry* 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ Params p,
                                                             const __grid_constant__ AttendArgs a,
                                                             const __grid_constant__ Plan plan, int slots, int max_ctas) {
+  __shared__ long long s_prefix[kPlanSlots + 1];
+  __shared__ int s_begin[kPlanSeqs + 1];
+  grid_launch_next();
   const int span = 2 * sub_tokens(p.G);
+  const int* q_begin = a.q_begin;
+  if (q_begin && p.B <= kPlanSeqs) {
+    for (int b = threadIdx.x; b <= p.B; b += kPlanThreads) s_begin[b] = q_begin[b];
+    q_begin = s_begin;
+    __syncthreads();
+  }
+  long long* prefix = slots <= kPlanSlots ? s_prefix : plan.prefix;
   long long sum = 0;
   for (int base = 0; base < slots; base += kPlanThreads) {
     const int slot = base + threadIdx.x;
     Tile t = {};
     if (slot < slots) {
       if (a.q_begin) {
-        t = prompt_tile(p, a, slot, span);
+        t = prompt_tile(p, a, q_begin, slot, span);
       } else if (slot < a.n_members) {  // own tokens of entry `slot`
         Entry e;
         const bool ok = group_entry(p, a, slot, &e);
@@ -226,7 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     long long total;
     const long long at = sum + plan_scan<long long>(t.blocks, &total);
-    if (slot < slots) plan.prefix[slot] = at;
+    if (slot < slots) plan.prefix[slot] = prefix[slot] = at;
     sum += total;
   }
   if (threadIdx.x == 0) plan.prefix[slots] = sum;
@@ -234,17 +250,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const long long units = sum * p.Hkv;
   const int ctas = static_cast<int>(min(static_cast<long long>(max_ctas), units));
   if (threadIdx.x == 0) *plan.head = PlanHead{sum, slots, ctas};
-  for (int c = threadIdx.x; c < ctas; c += kPlanThreads) {
+  for (int c = threadIdx.x; c < max_ctas; c += kPlanThreads) {
+    if (c >= ctas) {
+      plan.start[c] = Start{0, 0, 0, slots, 0, 0, {}};
+      continue;
+    }
     const long long g = first_unit(units, ctas, c);
     const int head = static_cast<int>(g / sum);
     const long long r = g - head * sum;
     int lo = 0, hi = slots - 1;  // the last tile that begins at or before r: not an empty one
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (plan.prefix[mid] <= r) lo = mid;
+      if (prefix[mid] <= r) lo = mid;
       else hi = mid - 1;
     }
-    plan.start[c] = Start{head, lo, static_cast<int>(r - plan.prefix[lo]), 0};
+    plan.start[c] = Start{head, lo, static_cast<int>(r - prefix[lo]), slots, first_unit(units, ctas, c + 1) - g, 0,
+                          plan.tile[lo]};
   }
 }
 
@@ -268,19 +289,14 @@ struct Walk {
   int count, head, tile, off;
   Tile ahead;  // tile `tile`, on its way before it is needed
 
-  __device__ Walk(const Plan& plan, int kv_heads, int c) : tiles(plan.tile) {
-    const PlanHead h = *plan.head;
-    count = h.tiles;
-    left = 0;
-    if (c < h.ctas) {
-      const long long units = h.per_head * kv_heads;
-      left = first_unit(units, h.ctas, c + 1) - first_unit(units, h.ctas, c);
-      const Start s = plan.start[c];
-      head = s.head;
-      tile = s.tile;
-      off = s.off;
-      ahead = tiles[tile];
-    }
+  __device__ Walk(const Plan& plan, int c) : tiles(plan.tile) {
+    const Start s = plan.start[c];
+    left = s.left;
+    count = s.count;
+    head = s.head;
+    tile = s.tile;
+    off = s.off;
+    ahead = s.first;
   }
 
   __device__ __forceinline__ bool next(Piece* x) {
@@ -423,7 +439,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
   volatile int* abort = &bars.abort;
-  Walk walk(plan, p.Hkv, blockIdx.x);
+  grid_wait();
+  Walk walk(plan, blockIdx.x);
   Piece x;
   bool ok = true;
 
@@ -656,8 +673,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       // one past the last token this row reads, from the piece's first; rows of no one read all
       int lim = !mine ? kNoMask : (x.t.pos0 == kNoMask ? x.t.kv1 : x.t.pos0 + t * tps + tok + 1) -
                                       (x.t.kv0 + x.b0 * kBlock);
+      int least = __reduce_min_sync(0xFFFFFFFFu, lim);  // of the warp's rows
       float m = -INFINITY, sum = 0.f;
-      for (int j = 0; j < n; ++j, lim -= kStep, ++step) {
+      for (int j = 0; j < n; ++j, lim -= kStep, least -= kStep, ++step) {
         const uint32_t buf = step & 1;
         ok = role_wait(&bars.s_full[t][buf], (step >> 1) & 1, abort, p.status);
         if (!ok) break;
@@ -669,8 +687,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           tmem_ld32(tB + 32, s + 32);
           tmem_wait_ld32(s);
           tmem_wait_ld32(s + 32);
-          const bool cut = __any_sync(0xFFFFFFFFu, lim < kStep);
-          if (cut) {
+          if (least < kStep) {
 #pragma unroll
             for (int c = 0; c < kStep; ++c)
               if (c >= lim) s[c] = -INFINITY;
@@ -773,6 +790,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     }
   }
   __syncthreads();
+  grid_launch_next();
   if (warp == 8) {
     tc_fence_after();
     tmem_free(tmem, TMEM_COLS);
@@ -781,32 +799,70 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
 // ------------------------------------------------------------------ merging partials
 
-// Merge the n partial rows that row_of(i) names and write the result; one warp.
+constexpr int kMergeWarps = 4;
+
+// Merge the n partial rows that row_of(i) names and write the result; one CTA, its warps
+// taking every kMergeWarps-th row, with the loads of four rows under way at a time.
 template <int D, typename RowOf>
 __device__ void merge_rows(const Plan& plan, const AttendArgs& a, int n, size_t at, RowOf row_of) {
   constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, plan.part[row_of(i) * (D + 4)]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float sum = 0.f, acc[C];
+  __shared__ float s_m[kMergeWarps], s_sum[kMergeWarps], s_acc[kMergeWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = -INFINITY, sum = 0.f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float* r = plan.part + row_of(i) * (D + 4);
-    const float f = r[0] == -INFINITY ? 0.f : exp2f(r[0] - m);
-    sum += r[1] * f;
+  for (int i0 = warp; i0 < n; i0 += 4 * kMergeWarps) {
+    float rm[4], rs[4], ro[4][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] += r[4 + lane * C + c] * f;
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kMergeWarps;
+      rm[u] = -INFINITY;
+      if (i < n) {
+        const float* r = plan.part + row_of(i) * (D + 4);
+        rm[u] = r[0];
+        rs[u] = r[1];
+#pragma unroll
+        for (int c = 0; c < C; ++c) ro[u][c] = r[4 + lane * C + c];
+      }
+    }
+    const float m1 = fmaxf(m, fmaxf(fmaxf(rm[0], rm[1]), fmaxf(rm[2], rm[3])));
+    if (m1 == -INFINITY) continue;
+    const float f = exp2f(m - m1);
+    m = m1;
+    sum *= f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (rm[u] == -INFINITY) continue;  // nothing there: the rest of the row may hold anything
+      const float g = exp2f(rm[u] - m);
+      sum += rs[u] * g;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += ro[u][c] * g;
+    }
+  }
+  __syncthreads();  // the row before has been read
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_sum[warp] = sum;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) s_acc[warp][lane * C + c] = acc[c];
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  m = s_m[0];
+  for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w]);
+  float x = 0.f, y = 0.f;
+  sum = 0.f;
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - m);
+    sum += s_sum[w] * f;
+    x += s_acc[w][2 * threadIdx.x] * f;
+    y += s_acc[w][2 * threadIdx.x + 1] * f;
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t w[C / 2];
-#pragma unroll
-  for (int c = 0; c < C; c += 2) w[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
-#pragma unroll
-  for (int c = 0; c < C / 2; ++c) reinterpret_cast<uint32_t*>(a.out + at * D + lane * C)[c] = w[c];
-  if (a.lse && lane == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  reinterpret_cast<uint32_t*>(a.out + at * D)[threadIdx.x] = pack_bf16(x * inv, y * inv);
+  if (a.lse && threadIdx.x == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // The CTAs that have units [z0, z1): [*c0, *c1].
@@ -821,10 +877,11 @@ __device__ __forceinline__ void ctas_of(long long units, int ctas, long long z0,
 
 // Packed prompts: CTA column c merges the tile that was cut first at the start of CTA c's run.
 template <int D>
-__global__ void __launch_bounds__(256) combine_tiles_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(32 * kMergeWarps) combine_tiles_kernel(const __grid_constant__ Params p,
                                                             const __grid_constant__ AttendArgs a,
                                                             const __grid_constant__ Plan plan) {
   const int c = blockIdx.x + 1;
+  grid_wait();
   const PlanHead h = *plan.head;
   if (c >= h.ctas) return;
   const Start s = plan.start[c];
@@ -836,7 +893,7 @@ __global__ void __launch_bounds__(256) combine_tiles_kernel(const __grid_constan
   int last = c;
   while (last + 1 < h.ctas && first_unit(units, h.ctas, last + 1) < z0 + t.blocks) ++last;
   const int tps = sub_tokens(p.G), n = last - c + 2;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < t.ntok * p.G; r += gridDim.y * 8) {
+  for (int r = blockIdx.y; r < t.ntok * p.G; r += gridDim.y) {
     const int tok = r / p.G, g = r % p.G;
     const int prow = tok / tps * kBlock + (tok % tps) * p.G + g;
     const size_t at = static_cast<size_t>(t.row0 + tok) * p.Hq + s.head * p.G + g;
@@ -846,17 +903,18 @@ __global__ void __launch_bounds__(256) combine_tiles_kernel(const __grid_constan
   }
 }
 
-// A batch in groups: one warp per (entry, query head) merges its prefix and its own tokens.
+// A batch in groups: one CTA per (entry, query head) merges its prefix and its own tokens.
 template <int D>
-__global__ void __launch_bounds__(256) combine_entries_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(32 * kMergeWarps) combine_entries_kernel(const __grid_constant__ Params p,
                                                               const __grid_constant__ AttendArgs a,
                                                               const __grid_constant__ Plan plan) {
-  const int i = blockIdx.x, head = blockIdx.y, g = threadIdx.x >> 5;
+  const int i = blockIdx.x, hq = blockIdx.y, head = hq / p.G, g = hq % p.G;
+  grid_wait();
   const int row = plan.row[i];
   if (row < 0) return;
   const PlanHead h = *plan.head;
   const long long units = h.per_head * p.Hkv;
-  const int tps = sub_tokens(p.G), hq = head * p.G + g;
+  const int tps = sub_tokens(p.G);
   int c0[2] = {0, 0}, n[2] = {0, 0};
   size_t first[2], later[2];
   // the entry's own tile, and the prefix tile that leads it
@@ -920,14 +978,13 @@ cudaError_t launch_attend_t(const Params& p, const AttendArgs& a, const CUtensor
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(attend_kernel<D>));
   if (e == cudaSuccess) e = launch_kernel(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, 0, p, a, plan, slots, ctas);
   if (e == cudaSuccess)
-    e = launch_kernel(attend_kernel<D>, dim3(ctas), dim3(kAttendThreads), Smem<D>::BYTES + 1024, s, 0, qmap, kmap,
-                      vmap, p, a, plan);
+    e = launch_kernel_early(attend_kernel<D>, dim3(ctas), dim3(kAttendThreads), Smem<D>::BYTES + 1024, s, qmap, kmap, vmap,
+                            p, a, plan);
   if (e != cudaSuccess) return e;
-  if (a.q_begin) {
-    if (ctas == 1) return e;
-    return launch_kernel(combine_tiles_kernel<D>, dim3(ctas - 1, 32), dim3(256), 0, s, 0, p, a, plan);
-  }
-  return launch_kernel(combine_entries_kernel<D>, dim3(a.n_members, p.Hkv), dim3(32 * p.G), 0, s, 0, p, a, plan);
+  if (!a.q_begin)
+    return launch_kernel_early(combine_entries_kernel<D>, dim3(a.n_members, p.Hq), dim3(32 * kMergeWarps), 0, s, p, a, plan);
+  if (ctas == 1) return e;
+  return launch_kernel_early(combine_tiles_kernel<D>, dim3(ctas - 1, 64), dim3(32 * kMergeWarps), 0, s, p, a, plan);
 }
 
 }  // namespace

@@ -24,6 +24,10 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Let the stream's next kernel start (it waits for this one's results with grid_wait) / wait for the kernel before.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The barrier gets one arrival once all tcgen05 work this thread has issued is done.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -157,30 +161,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// 2^y for y in [-inf, 128) on the multiply-add units, which the exponential unit leaves idle, two values
-// at a time and in steps, so that callers can interleave several: y = n + f with n the nearest
-// integer, 2^f by the degree-4 polynomial with constant term 1 whose largest relative error on
-// [-1/2, 1/2] is smallest (2.9e-06), n added to the exponent.  Below -125: 2^-125.
-struct Exp2Poly {
-  float2 y, t, p;
-  static constexpr int kSteps = 8;
-  __device__ __forceinline__ void step(int i) {
-    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-    if (i == 0) y = make_float2(fmaxf(y.x, -125.f), fmaxf(y.y, -125.f));
-    if (i == 1) t = add2(y, make_float2(kBig, kBig));
-    if (i == 2) p = add2(t, make_float2(-kBig, -kBig));
-    if (i == 3) y = fma2(p, make_float2(-1.f, -1.f), y);
-    if (i == 4) p = fma2(y, make_float2(0.009582853f, 0.009582853f), make_float2(0.055906426f, 0.055906426f));
-    if (i == 5) p = fma2(p, y, make_float2(0.24024099f, 0.24024099f));
-    if (i == 6) p = fma2(p, y, make_float2(0.6931242f, 0.6931242f));
-    if (i == 7) {
-      p = fma2(p, y, make_float2(1.f, 1.f));
-      y = make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-    }
-  }
-};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t w;
