@@ -53,7 +53,8 @@ constexpr int kNoMask = 1 << 30;
 struct Start {  // a CTA's run: where it begins, how long it is, and its first tile
   int head, tile, off, count;  // count: tiles of the plan
   long long left;
-  long long pad;
+  int pieces;  // of that tile, where this is the first cut through it: its pieces are of CTAs c - 1, c, ...; else 0
+  int pad;
   Tile first;
 };
 
@@ -73,6 +74,10 @@ struct Plan {
 };
 
 __host__ __device__ inline long long first_unit(long long units, int ctas, int c) { return units * c / ctas; }
+// The CTA whose run has unit z: the last with first_unit <= z.
+__device__ __forceinline__ int cta_of(long long units, int ctas, long long z) {
+  return static_cast<int>(((z + 1) * ctas - 1) / units);
+}
 
 // ------------------------------------------------------------------ the plan
 
@@ -264,8 +269,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (prefix[mid] <= r) lo = mid;
       else hi = mid - 1;
     }
-    plan.start[c] = Start{head, lo, static_cast<int>(r - prefix[lo]), slots, first_unit(units, ctas, c + 1) - g, 0,
-                          plan.tile[lo]};
+    const Tile t = plan.tile[lo];
+    const int off = static_cast<int>(r - prefix[lo]);
+    const int pieces = off > 0 && cta_of(units, ctas, g - off) == c - 1
+                           ? cta_of(units, ctas, g - off + t.blocks - 1) - c + 2 : 0;
+    plan.start[c] = Start{head, lo, off, slots, first_unit(units, ctas, c + 1) - g, pieces, 0, t};
   }
 }
 
@@ -329,15 +337,16 @@ struct Smem {
   static constexpr int Q_SLAB = 128 * 128;        // 64 channels of them
   static constexpr int TILE = kStep * D * 2;      // K or V of one step
   static constexpr int SLAB = kStep * 128;
-  static constexpr int STAGES = D == 128 ? 10 : 20;
+  static constexpr int STAGES = D == 128 ? 9 : 18;
   static constexpr int Q = 0;
   static constexpr int KV = 2 * Q_TILE;
-  static constexpr int BARS = KV + STAGES * TILE;
+  static constexpr int OUT = KV + STAGES * TILE;  // 32 rows of 64 bytes for each softmax warp
+  static constexpr int BARS = OUT + 8 * 2048;
   static constexpr int BYTES = BARS + 768;
 };
 
 struct Bars {
-  uint64_t full[20], empty[20], clean[20];  // of the stages; clean: rows of V past the last token are zero
+  uint64_t full[18], empty[18], clean[18];  // of the stages; clean: rows of V past the last token are zero
   uint64_t s_full[2][2], p_full[2][2];  // [rows t][buffer]
   uint64_t q_full[2], q_free[2], o_step[2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
@@ -755,8 +764,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const size_t at = static_cast<size_t>(row < 0 ? 0 : row) * p.Hq + hq;
         // partial rows: of the CTA (a tile's later pieces; of a prompt also its first), or of the batch
-        const size_t prow = !x.first ? (2ull * blockIdx.x) * 256 + t * kBlock + tid
-                            : a.q_begin ? (2ull * blockIdx.x + 1) * 256 + t * kBlock + tid
+        const size_t prow = !x.first ? (2ull * blockIdx.x) * 256 + t * 128 + tid
+                            : a.q_begin ? (2ull * blockIdx.x + 1) * 256 + t * 128 + tid
                                         : 2ull * kMaxAttendCtas * 256 + x.t.part0 +
                                               static_cast<size_t>(t * tps + tok) * p.Hq + hq;
         float* part = plan.part + prow * (D + 4);
@@ -766,21 +775,48 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           part[0] = m;
           part[1] = sum;
         }
+        // Each thread has one row; 64 bytes of the warp's rows at a time go through shared memory, so
+        // that four threads store 64 consecutive bytes of a row.
+        unsigned char* box = smem + L::OUT + warp * 2048;
+        char* own = row < 0 ? nullptr : direct ? reinterpret_cast<char*>(a.out + at * D) : reinterpret_cast<char*>(part + 4);
+        char* to[4];
 #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[i] = reinterpret_cast<char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(own), 8 * i + lane / 4));
+        auto store64 = [&](const uint4 (&w)[4], int offset) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = w[i];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + lane / 4;
+            const uint4 v = *reinterpret_cast<const uint4*>(box + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+            if (to[i]) *reinterpret_cast<uint4*>(to[i] + offset + (lane & 3) * 16) = v;
+          }
+        };
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(tO + c, o);
           tmem_wait_ld32(o);
-          if (row >= 0 && direct) {
+          uint4 w[4];
+          if (direct) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(a.out + at * D + c + i) =
-                  make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                             pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
-          } else if (row >= 0) {
+            for (int i = 0; i < 4; ++i)
+              w[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            store64(w, c * 2);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(part + 4 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = make_uint4(__float_as_uint(o[16 * h + 4 * i]), __float_as_uint(o[16 * h + 4 * i + 1]),
+                                  __float_as_uint(o[16 * h + 4 * i + 2]), __float_as_uint(o[16 * h + 4 * i + 3]));
+              store64(w, c * 4 + h * 64);
+            }
           }
         }
       }
@@ -801,10 +837,47 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
 constexpr int kMergeWarps = 4;
 
-// Merge the n partial rows that row_of(i) names and write the result; one CTA, its warps
-// taking every kMergeWarps-th row, with the loads of four rows under way at a time.
+// Merge the n partial rows that row_of(i) names and write the result.  Few rows: one warp
+// (rows of different warps are different results).
+template <int D, int kFewRows, typename RowOf>
+__device__ void merge_few(const Plan& plan, const AttendArgs& a, int n, size_t at, RowOf row_of) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  float rm[kFewRows], rs[kFewRows], ro[kFewRows][C];
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i) {
+    rm[i] = -INFINITY;
+    if (i < n) {
+      const float* r = plan.part + row_of(i) * (D + 4);
+      rm[i] = r[0];
+      rs[i] = r[1];
+#pragma unroll
+      for (int c = 0; c < C; ++c) ro[i][c] = r[4 + lane * C + c];
+    }
+  }
+  float m = rm[0], sum = 0.f, acc[C];
+#pragma unroll
+  for (int i = 1; i < kFewRows; ++i) m = fmaxf(m, rm[i]);
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i) {
+    if (rm[i] == -INFINITY) continue;  // nothing there: the rest of the row may hold anything
+    const float f = exp2f(rm[i] - m);
+    sum += rs[i] * f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += ro[i][c] * f;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int c = 0; c < C; c += 2)
+    reinterpret_cast<uint32_t*>(a.out + at * D + lane * C)[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+  if (a.lse && lane == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Many rows: one CTA, its warps taking every kMergeWarps-th, with the loads of four rows under way at a time.
 template <int D, typename RowOf>
-__device__ void merge_rows(const Plan& plan, const AttendArgs& a, int n, size_t at, RowOf row_of) {
+__device__ void merge_many(const Plan& plan, const AttendArgs& a, int n, size_t at, RowOf row_of) {
   constexpr int C = D / 32;
   __shared__ float s_m[kMergeWarps], s_sum[kMergeWarps], s_acc[kMergeWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -865,16 +938,6 @@ __device__ void merge_rows(const Plan& plan, const AttendArgs& a, int n, size_t 
   if (a.lse && threadIdx.x == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// The CTAs that have units [z0, z1): [*c0, *c1].
-__device__ __forceinline__ void ctas_of(long long units, int ctas, long long z0, long long z1, int* c0, int* c1) {
-  int lo = static_cast<int>(z0 * ctas / units);
-  while (lo + 1 < ctas && first_unit(units, ctas, lo + 1) <= z0) ++lo;
-  int hi = lo;
-  while (hi + 1 < ctas && first_unit(units, ctas, hi + 1) < z1) ++hi;
-  *c0 = lo;
-  *c1 = hi;
-}
-
 // Packed prompts: CTA column c merges the tile that was cut first at the start of CTA c's run.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) combine_tiles_kernel(const __grid_constant__ Params p,
@@ -882,70 +945,79 @@ __global__ void __launch_bounds__(32 * kMergeWarps) combine_tiles_kernel(const _
                                                             const __grid_constant__ Plan plan) {
   const int c = blockIdx.x + 1;
   grid_wait();
-  const PlanHead h = *plan.head;
-  if (c >= h.ctas) return;
   const Start s = plan.start[c];
-  if (s.off == 0) return;
-  const long long units = h.per_head * p.Hkv;
-  const Tile t = plan.tile[s.tile];
-  const long long z0 = first_unit(units, h.ctas, c) - s.off;
-  if (first_unit(units, h.ctas, c - 1) > z0) return;  // an earlier column has this tile
-  int last = c;
-  while (last + 1 < h.ctas && first_unit(units, h.ctas, last + 1) < z0 + t.blocks) ++last;
-  const int tps = sub_tokens(p.G), n = last - c + 2;
-  for (int r = blockIdx.y; r < t.ntok * p.G; r += gridDim.y) {
+  const int n = s.pieces, tps = sub_tokens(p.G);
+  if (n == 0) return;
+  const Tile& t = s.first;
+  constexpr int kFewRows = 4;
+  const bool few = n <= kFewRows;
+  const int warp = few ? threadIdx.x >> 5 : 0, warps = few ? kMergeWarps : 1;
+  for (int r = blockIdx.y * warps + warp; r < t.ntok * p.G; r += gridDim.y * warps) {
     const int tok = r / p.G, g = r % p.G;
-    const int prow = tok / tps * kBlock + (tok % tps) * p.G + g;
+    const int prow = tok / tps * 128 + (tok % tps) * p.G + g;
     const size_t at = static_cast<size_t>(t.row0 + tok) * p.Hq + s.head * p.G + g;
-    merge_rows<D>(plan, a, n, at, [&](int i) {
-      return (i == 0 ? 2ull * (c - 1) + 1 : 2ull * (c + i - 1)) * 256 + prow;
-    });
+    auto row_of = [&](int i) { return (i == 0 ? 2ull * (c - 1) + 1 : 2ull * (c + i - 1)) * 256 + prow; };
+    if (few) merge_few<D, kFewRows>(plan, a, n, at, row_of);
+    else merge_many<D>(plan, a, n, at, row_of);
   }
 }
 
-// A batch in groups: one CTA per (entry, query head) merges its prefix and its own tokens.
+// A batch in groups: each query head of an entry is merged from its prefix and its own tokens, by a CTA, or by
+// a warp where there are few pieces (the CTAs left over end).
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) combine_entries_kernel(const __grid_constant__ Params p,
-                                                              const __grid_constant__ AttendArgs a,
-                                                              const __grid_constant__ Plan plan) {
-  const int i = blockIdx.x, hq = blockIdx.y, head = hq / p.G, g = hq % p.G;
+                                                                           const __grid_constant__ AttendArgs a,
+                                                                           const __grid_constant__ Plan plan) {
+  const int i = blockIdx.x;
   grid_wait();
   const int row = plan.row[i];
   if (row < 0) return;
   const PlanHead h = *plan.head;
   const long long units = h.per_head * p.Hkv;
   const int tps = sub_tokens(p.G);
-  int c0[2] = {0, 0}, n[2] = {0, 0};
-  size_t first[2], later[2];
-  // the entry's own tile, and the prefix tile that leads it
-  int lead = -1;
-  {
-    int lo = 0, hi = a.n_groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.group_begin[mid] <= i) lo = mid;
-      else hi = mid - 1;
-    }
-    const int g0 = a.group_begin[lo];
-    lead = i - (i - g0) % (2 * tps);
+  // the entry's prefix tile is the slot of the entry that leads it
+  int lo = 0, hi = a.n_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.group_begin[mid] <= i) lo = mid;
+    else hi = mid - 1;
   }
+  const int lead = i - (i - a.group_begin[lo]) % (2 * tps);
   const int slot[2] = {a.n_members + lead, i};
+  const Tile tile[2] = {plan.tile[slot[0]], plan.tile[slot[1]]};
+  auto merge = [&](int hq, auto&& how) {
+    const int head = hq / p.G, g = hq % p.G;
+    int c0[2] = {0, 0}, n[2] = {0, 0};
+    size_t first[2], later[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const Tile t = plan.tile[slot[k]];
-    if (t.blocks == 0) continue;
-    const long long z0 = head * h.per_head + plan.prefix[slot[k]];
-    int c1;
-    ctas_of(units, h.ctas, z0, z0 + t.blocks, &c0[k], &c1);
-    n[k] = c1 - c0[k] + 1;
-    const int tok = i - t.row0;
-    first[k] = 2ull * kMaxAttendCtas * 256 + t.part0 + static_cast<size_t>(tok) * p.Hq + hq;
-    later[k] = tok / tps * kBlock + (tok % tps) * p.G + g;
+    for (int k = 0; k < 2; ++k) {
+      const Tile& t = tile[k];
+      if (t.blocks == 0) continue;
+      const long long z0 = head * h.per_head + plan.prefix[slot[k]];
+      c0[k] = cta_of(units, h.ctas, z0);
+      n[k] = cta_of(units, h.ctas, z0 + t.blocks - 1) - c0[k] + 1;
+      const int tok = i - t.row0;
+      first[k] = 2ull * kMaxAttendCtas * 256 + t.part0 + static_cast<size_t>(tok) * p.Hq + hq;
+      later[k] = tok / tps * 128 + (tok % tps) * p.G + g;
+    }
+    how(n[0] + n[1], static_cast<size_t>(row) * p.Hq + hq, [&](int j) {
+      const int k = j < n[0] ? 0 : 1, piece = k ? j - n[0] : j;
+      return piece == 0 ? first[k] : 2ull * (c0[k] + piece) * 256 + later[k];
+    });
+  };
+  // no head has more pieces than this
+  const long long run = units > 0 ? max(units / h.ctas, 1ll) : 1;
+  long long most = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) most += tile[k].blocks ? (tile[k].blocks - 1) / run + 2 : 0;
+  constexpr int kFewRows = 8;
+  const bool few = most <= kFewRows;
+  if (few) {
+    const int hq = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+    if (hq < p.Hq) merge(hq, [&](int n, size_t at, auto&& row_of) { merge_few<D, kFewRows>(plan, a, n, at, row_of); });
+  } else {
+    merge(blockIdx.y, [&](int n, size_t at, auto&& row_of) { merge_many<D>(plan, a, n, at, row_of); });
   }
-  merge_rows<D>(plan, a, n[0] + n[1], static_cast<size_t>(row) * p.Hq + hq, [&](int j) {
-    const int k = j < n[0] ? 0 : 1, piece = k ? j - n[0] : j;
-    return piece == 0 ? first[k] : 2ull * (c0[k] + piece) * 256 + later[k];
-  });
 }
 
 // ------------------------------------------------------------------ launches
@@ -984,7 +1056,7 @@ cudaError_t launch_attend_t(const Params& p, const AttendArgs& a, const CUtensor
   if (!a.q_begin)
     return launch_kernel_early(combine_entries_kernel<D>, dim3(a.n_members, p.Hq), dim3(32 * kMergeWarps), 0, s, p, a, plan);
   if (ctas == 1) return e;
-  return launch_kernel_early(combine_tiles_kernel<D>, dim3(ctas - 1, 64), dim3(32 * kMergeWarps), 0, s, p, a, plan);
+  return launch_kernel_early(combine_tiles_kernel<D>, dim3(ctas - 1, 32), dim3(32 * kMergeWarps), 0, s, p, a, plan);
 }
 
 }  // namespace
