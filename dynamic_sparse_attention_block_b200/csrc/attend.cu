@@ -289,6 +289,8 @@ struct Piece {
   __device__ __forceinline__ int steps() const {  // of kStep tokens
     return (min(t.kv1 - t.kv0, b1 * kBlock) - b0 * kBlock + kStep - 1) / kStep;
   }
+  // Up to 128 rows: both halves take them, half t every other step from t on, and merge at the end.
+  __device__ __forceinline__ bool split(int tps) const { return t.ntok <= tps; }
 };
 
 struct Walk {
@@ -347,7 +349,8 @@ struct Smem {
 
 struct Bars {
   uint64_t full[18], empty[18], clean[18];  // of the stages; clean: rows of V past the last token are zero
-  uint64_t s_full[2][2], p_full[2][2];  // [rows t][buffer]
+  uint64_t s_full[2][2], p_full[2][2];  // [half t][buffer]
+  uint64_t xchg[4][2];                  // [warp of a half][half t]
   uint64_t q_full[2], q_free[2], o_step[2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
   int abort;
@@ -432,9 +435,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(&bars.q_free[t], 1);
       mbar_init(&bars.o_step[t], 1);
       mbar_init(&bars.o_full[t], 1);
-      mbar_init(&bars.o_free[t], 4);
+      mbar_init(&bars.o_free[t], 8);
       mbar_init(&bars.drain[t], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&bars.xchg[i >> 1][i & 1], 1);
     bars.abort = 0;
     fence_barrier_init();
     prefetch_tensormap(&kmap);
@@ -454,50 +458,59 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   bool ok = true;
 
   if (warp == 10) {
-    // ---------------------------------------------------------------- copies: K0 K1 V0 K2 V1 K3 ...
-    Ring<NS> ring;
-    long long fills = 0;
+    // ---------------------------------------------------------------- copies: K0 K1 V0 K2 V1 K3 ... (rounds)
+    // Each lane works out every 32nd copy, table look-up included, and they issue them in turn: a copy costs its
+    // wait and its issue only.
+    Ring<NS> ring, mine;  // mine: this lane's last copy
+    bool any = false;
+    const int bs_log2 = p.bs == 128 ? 7 : 6;
     while (ok && walk.next(&x)) {
       const int begin = x.t.kv0 + x.b0 * kBlock, n = x.steps();
-      int page[2] = {0, 0}, have[2] = {-1, -1};  // lane i: the page of cache block have + i; for K, for V
-      for (int i = 0; ok && i < 2 * n; ++i) {
-        const int kv = i == 0 || (i & 1 && i < 2 * n - 1) ? 0 : 1;  // one step of K ahead of V
-        const int j = kv ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2;
-        const int tok0 = begin + j * kStep;
+      const bool split = x.split(tps);
+      const int rounds = split ? (n + 1) / 2 : n;  // a round: a step for each half, or one for both
+      for (int base = 0; ok && base < 2 * n; base += 32) {
+        int i = base + lane, sub = 0;
+        if (split && n > 1) {
+          if ((n & 1) && i > 4 * rounds - 6) ++i;  // the last round is one step: K's has no second
+          sub = i & 1;
+          i >>= 1;
+        }
+        const bool v = !(i == 0 || (i & 1 && i < 2 * rounds - 1));  // one round of K ahead of V
+        const int round = v ? (i == 2 * rounds - 1 ? rounds - 1 : i / 2 - 1) : (i + 1) / 2;
+        const int tok0 = begin + (split ? 2 * round + sub : round) * kStep;
         int row = tok0, slice = x.t.seq * p.Hkv + x.head;
-        if (p.table) {
-          const int blk = tok0 / p.bs;
-          if (have[kv] < 0 || blk >= have[kv] + 32) {
-            have[kv] = blk;
-            page[kv] = blk + lane < (x.t.kv1 + p.bs - 1) / p.bs
-                           ? p.table[static_cast<size_t>(x.t.seq) * p.maxnb + blk + lane] : 0;
-          }
-          const int pg = __shfl_sync(0xFFFFFFFFu, page[kv], blk - have[kv]);
+        if (p.table && base + lane < 2 * n) {
+          const int blk = tok0 >> bs_log2;
+          const int pg = p.table[static_cast<size_t>(x.t.seq) * p.maxnb + blk];
           const bool good = pg >= 0 && pg < p.pages;
-          if (!good && lane == 0) report(p.status, kDevBadRange);
+          if (!good) report(p.status, kDevBadRange);
           slice = good ? pg * p.Hkv + x.head : p.pages * p.Hkv;  // past the map: zeros
-          row = tok0 - blk * p.bs;
+          row = tok0 - (blk << bs_log2);
         }
-        ok = role_wait(&bars.empty[ring.s], ring.ph ^ 1, abort, p.status);
-        if (!ok) break;
-        if (lane == 0) {
-          unsigned char* dst = smem + L::KV + ring.s * L::TILE;
-          mbar_expect_tx(&bars.full[ring.s], L::TILE);
+        const CUtensorMap* map = v ? &vmap : &kmap;
+        const int count = min(32, 2 * n - base);
+        for (int k = 0; k < count; ++k, ring.next()) {
+          if (lane == k) {
+            ok = thread_wait(&bars.empty[ring.s], ring.ph ^ 1, abort, p.status);
+            if (ok) {
+              unsigned char* dst = smem + L::KV + ring.s * L::TILE;
+              mbar_expect_tx(&bars.full[ring.s], L::TILE);
 #pragma unroll
-          for (int r = 0; r < NREG; ++r)
-            tma_load_3d(dst + r * L::SLAB, kv ? &vmap : &kmap, &bars.full[ring.s], r * 64, row, slice);
+              for (int r = 0; r < NREG; ++r) tma_load_3d(dst + r * L::SLAB, map, &bars.full[ring.s], r * 64, row, slice);
+              mine = ring;
+              any = true;
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        ++fills;
-        ring.next();
+        ok = __all_sync(0xFFFFFFFFu, ok);
       }
     }
-    // copies still in flight land before the CTA ends (all have, unless a wait ran out)
-    if (*abort && lane == 0)
-      for (long long f = max(0ll, fills - NS); f < fills; ++f)
-        mbar_wait(&bars.full[f % NS], static_cast<uint32_t>(f / NS) & 1, p.status);
+    // copies still in flight (the last of some lanes) land before the CTA ends; all have, unless a wait ran out
+    if (*abort && any) mbar_wait(&bars.full[mine.s], mine.ph, p.status);
+    __syncwarp();
   } else if (warp >= 8 && warp < 10) {
-    // ---------------------------------------------------------------- products of rows t, by one thread
+    // ---------------------------------------------------------------- products of half t, by one thread
     const int t = warp - 8;
     // a negative scale negates Q, so that the largest product has the largest logit
     const uint32_t QK = mma_desc(128, kStep, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
@@ -522,63 +535,90 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       for (int k = 0; k < kStep / 16; ++k) mma_ts(d, pt + k * 8, v0 + k * 128, PV, add || k > 0);
     };
     if (elect_one()) {
+      Ring<NS> other;  // a stage of the other half, still to be let pass
+      bool owes = false;
+      int last = 0;    // the last stage of the round taken last
       while (ok && walk.next(&x)) {
-        const int halves = x.t.ntok > tps ? 2 : 1, n = x.steps();
+        const int n = x.steps();
+        const bool split = x.split(tps);
+        const int rounds = split ? (n + 1) / 2 : n, mine = split ? (n + 1 - t) / 2 : n;
         const bool tail = (x.t.kv1 - x.t.kv0 - x.b0 * kBlock) - (n - 1) * kStep < kStep;
-        if (t >= halves) {  // nothing here: let the stages pass
-          for (int i = 0; ok && i < 2 * n; ++i, ring.next()) {
-            ok = thread_wait(&bars.full[ring.s], ring.ph, abort, p.status);
-            if (ok) mbar_arrive(&bars.empty[ring.s]);
-            if (tail && i == 2 * n - 1) cph ^= 1u << ring.s;
+        auto pass = [&](const Ring<NS>& r) {
+          ok = ok && thread_wait(&bars.full[r.s], r.ph, abort, p.status);
+          if (ok) mbar_arrive(&bars.empty[r.s]);
+        };
+        // This half's stage of K or V round i, once it has landed.  The other half's stage passes: one ahead of it at
+        // once, one behind it before the next is taken.
+        auto take = [&](int i) {
+          if (owes) pass(other);
+          owes = false;
+          const bool two = split && 2 * i + 1 < n;
+          if (split && t == 1) {
+            pass(ring);
+            last = ring.s;
+            ring.next();
+            if (!two) return 0;
           }
-          continue;
-        }
+          const int stage = last = ring.s;
+          ok = ok && thread_wait(&bars.full[ring.s], ring.ph, abort, p.status);
+          ring.next();
+          if (two && t == 0) {
+            other = ring;
+            owes = true;
+            last = ring.s;
+            ring.next();
+          }
+          return stage;
+        };
         ok = thread_wait(&bars.q_full[t], qph, abort, p.status);
         qph ^= 1;
-        for (int j = 0; ok && j < min(2, n); ++j) {  // S of the first two steps
-          ok = thread_wait(&bars.full[ring.s], ring.ph, abort, p.status);
-          if (!ok) break;
+        if (mine == 0) mbar_arrive(&bars.q_free[t]);
+        for (int i = 0; ok && i < min(2, rounds); ++i) {  // S of the first two steps
+          const int k = take(i);
+          if (!ok || i >= mine) break;
           tc_fence_after();
-          qk(ring.s, asked & 1);
+          qk(k, asked & 1);
           tc_commit(&bars.s_full[t][asked & 1]);
-          if (j == n - 1) tc_commit(&bars.q_free[t]);
-          tc_commit(&bars.empty[ring.s]);
+          if (i == mine - 1) tc_commit(&bars.q_free[t]);
+          tc_commit(&bars.empty[k]);
           ++asked;
-          ring.next();
         }
         // the previous piece's O has been read
         ok = ok && thread_wait(&bars.o_free[t], fph, abort, p.status);
         fph ^= 1;
-        for (int j = 0; ok && j < n; ++j) {
-          const bool more = j + 2 < n;
+        for (int i = 0; ok && i < rounds; ++i) {
+          const bool more = i + 2 < mine;
           const uint32_t buf = used & 1;
-          const Ring<NS> v = ring;
-          ring.next();
-          const Ring<NS> k2 = ring;
-          if (more) ring.next();
-          ok = thread_wait(&bars.full[v.s], v.ph, abort, p.status);
-          if (ok && more) ok = thread_wait(&bars.full[k2.s], k2.ph, abort, p.status);
-          if (ok && j == n - 1 && tail) {
-            ok = thread_wait(&bars.clean[v.s], (cph >> v.s) & 1, abort, p.status);
-            cph ^= 1u << v.s;
+          const int v = take(i);
+          const int at = last;
+          const int k2 = i + 2 < rounds ? take(i + 2) : 0;
+          if (i == rounds - 1 && tail) {  // `at` is the piece's last stage
+            if (ok && (split ? 2 * i + t == n - 1 : true))
+              ok = thread_wait(&bars.clean[at], (cph >> at) & 1, abort, p.status);
+            cph ^= 1u << at;
           }
-          ok = ok && thread_wait(&bars.p_full[t][buf], (used >> 1) & 1, abort, p.status);
+          if (!ok || i >= mine) break;
+          ok = thread_wait(&bars.p_full[t][buf], (used >> 1) & 1, abort, p.status);
           if (!ok) break;
           tc_fence_after();
-          pv(v.s, buf, j > 0);
+          pv(v, buf, i > 0);
           tc_commit(&bars.o_step[t]);
           if (more) {
-            qk(k2.s, buf);  // runs behind the product that reads P there
+            qk(k2, buf);  // runs behind the product that reads P there
             tc_commit(&bars.s_full[t][buf]);
-            if (j + 3 == n) tc_commit(&bars.q_free[t]);
-            tc_commit(&bars.empty[k2.s]);
+            if (i + 3 == mine) tc_commit(&bars.q_free[t]);
+            tc_commit(&bars.empty[k2]);
             ++asked;
-          } else if (j == n - 1) {
+          } else if (i == mine - 1) {
             tc_commit(&bars.o_full[t]);
           }
-          tc_commit(&bars.empty[v.s]);
+          tc_commit(&bars.empty[v]);
           ++used;
         }
+      }
+      if (owes && ok) {
+        ok = thread_wait(&bars.full[other.s], other.ph, abort, p.status);
+        if (ok) mbar_arrive(&bars.empty[other.s]);
       }
       if (*abort) {  // products still in flight end before their memory is given back
         tc_commit(&bars.drain[t]);
@@ -608,8 +648,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     while (ok && walk.next(&x)) {
       const int n = x.steps();
       for (int t = 0; ok && t < 2; ++t) {
-        const int ntok = min(tps, x.t.ntok - t * tps);
-        if (ntok <= 0) break;
+        const int tok0 = x.split(tps) ? 0 : t * tps, ntok = min(tps, x.t.ntok - tok0);
         ok = role_wait(&bars.q_free[t], (fph >> t) & 1, abort, p.status);
         fph ^= 1u << t;
         if (ok && t == 0 && valid < kStep) clean();  // of the piece before
@@ -620,7 +659,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 #pragma unroll
             for (int r = 0; r < NREG; ++r)
               tma_load_3d(smem + L::Q + t * L::Q_TILE + r * L::Q_SLAB, &qmap, &bars.q_full[t], r * 64, x.head * G,
-                          x.t.row0 + t * tps);
+                          x.t.row0 + tok0);
           }
           __syncwarp();
           continue;
@@ -635,7 +674,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const int rows = ntok * G;
 #pragma unroll 4
         for (int r = lane / C; r < rows; r += STEP) {
-          const int row = plan.row[x.t.row0 + t * tps + tok];
+          const int row = plan.row[x.t.row0 + tok0 + tok];
           if (row >= 0)
             cp_async_16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                         q + static_cast<size_t>(row) * a.q_stride + static_cast<size_t>(g) * D);
@@ -673,18 +712,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const float2 sc = make_float2(scale, scale);
     uint32_t step = 0, oph = 0;  // steps of these rows, over all pieces
     while (ok && walk.next(&x)) {
-      const int ntok = min(tps, x.t.ntok - t * tps), n = x.steps();
-      if (ntok <= 0) continue;
+      const bool split = x.split(tps);
+      const int tok0 = split ? 0 : t * tps, ntok = min(tps, x.t.ntok - tok0);
+      const int n = split ? (x.steps() + 1 - t) / 2 : x.steps();  // steps of this half
       const bool mine = tok < ntok;
       const bool work = __any_sync(0xFFFFFFFFu, mine);
-      const int e = x.t.row0 + t * tps + (mine ? tok : 0);
+      const int e = x.t.row0 + tok0 + (mine ? tok : 0);
       const int row = !mine ? -1 : a.q_begin ? e : plan.row[e];
-      // one past the last token this row reads, from the piece's first; rows of no one read all
-      int lim = !mine ? kNoMask : (x.t.pos0 == kNoMask ? x.t.kv1 : x.t.pos0 + t * tps + tok + 1) -
-                                      (x.t.kv0 + x.b0 * kBlock);
+      // one past the last token this row reads, from this half's next step; rows of no one read all
+      int lim = !mine ? kNoMask : (x.t.pos0 == kNoMask ? x.t.kv1 : x.t.pos0 + tok0 + tok + 1) -
+                                      (x.t.kv0 + x.b0 * kBlock) - (split ? t * kStep : 0);
+      const int stride = split ? 2 * kStep : kStep;
       int least = __reduce_min_sync(0xFFFFFFFFu, lim);  // of the warp's rows
       float m = -INFINITY, sum = 0.f;
-      for (int j = 0; j < n; ++j, lim -= kStep, least -= kStep, ++step) {
+      for (int j = 0; j < n; ++j, lim -= stride, least -= stride, ++step) {
         const uint32_t buf = step & 1;
         ok = role_wait(&bars.s_full[t][buf], (step >> 1) & 1, abort, p.status);
         if (!ok) break;
@@ -754,30 +795,57 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[t][buf]);
       }
-      ok = ok && role_wait(&bars.o_full[t], oph, abort, p.status);
-      oph ^= 1;
+      if (n > 0) {
+        ok = ok && role_wait(&bars.o_full[t], oph, abort, p.status);
+        oph ^= 1;
+      }
       if (!ok) break;
       tc_fence_after();
+      unsigned char* box = smem + L::OUT + warp * 2048;
+      float f = 1.f, fo = 0.f;  // factors of this half's and the other half's O, in a split piece
+      if (split) {              // (by warps without rows too: none gets a piece ahead of its partner)
+        uint64_t* here = &bars.xchg[warp & 3][t];
+        uint64_t* there = &bars.xchg[warp & 3][t ^ 1];
+        reinterpret_cast<float2*>(box)[lane] = make_float2(m, sum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(there);
+        ok = role_wait(here, 0, abort, p.status);
+        if (!ok) break;
+        tc_fence_after();  // the other half's O is complete too
+        const float2 o = reinterpret_cast<const float2*>(smem + L::OUT + (warp ^ 4) * 2048)[lane];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(there);
+        const float both = fmaxf(m, o.x);
+        f = m == -INFINITY ? 0.f : exp2_fast(m - both);
+        fo = o.x == -INFINITY ? 0.f : exp2_fast(o.x - both);
+        m = both;
+        sum = sum * f + o.y * fo;
+        ok = role_wait(here, 1, abort, p.status);  // the other half has read the box
+        if (!ok) break;
+      }
       if (work) {
         const int hq = x.head * G + g;
         const bool direct = a.q_begin && x.whole;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const size_t at = static_cast<size_t>(row < 0 ? 0 : row) * p.Hq + hq;
         // partial rows: of the CTA (a tile's later pieces; of a prompt also its first), or of the batch
-        const size_t prow = !x.first ? (2ull * blockIdx.x) * 256 + t * 128 + tid
-                            : a.q_begin ? (2ull * blockIdx.x + 1) * 256 + t * 128 + tid
+        const int prow0 = (split ? 0 : t * 128) + tid;
+        const size_t prow = !x.first ? (2ull * blockIdx.x) * 256 + prow0
+                            : a.q_begin ? (2ull * blockIdx.x + 1) * 256 + prow0
                                         : 2ull * kMaxAttendCtas * 256 + x.t.part0 +
-                                              static_cast<size_t>(t * tps + tok) * p.Hq + hq;
+                                              static_cast<size_t>(tok0 + tok) * p.Hq + hq;
         float* part = plan.part + prow * (D + 4);
-        if (row >= 0 && direct) {
-          if (a.lse) a.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
-        } else if (row >= 0) {
-          part[0] = m;
-          part[1] = sum;
+        if (row >= 0 && !(split && t == 1)) {
+          if (!direct) {
+            part[0] = m;
+            part[1] = sum;
+          } else if (a.lse) {
+            a.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
+          }
         }
         // Each thread has one row; 64 bytes of the warp's rows at a time go through shared memory, so
         // that four threads store 64 consecutive bytes of a row.
-        unsigned char* box = smem + L::OUT + warp * 2048;
         char* own = row < 0 ? nullptr : direct ? reinterpret_cast<char*>(a.out + at * D) : reinterpret_cast<char*>(part + 4);
         char* to[4];
 #pragma unroll
@@ -795,11 +863,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (to[i]) *reinterpret_cast<uint4*>(to[i] + offset + (lane & 3) * 16) = v;
           }
         };
+        // (of a split piece half the columns each)
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = split ? t * (D / 2) : 0; c < (split ? (t + 1) * (D / 2) : D); c += 32) {
           float o[32];
           tmem_ld32(tO + c, o);
           tmem_wait_ld32(o);
+          if (split) {
+            float q[32];
+            tmem_ld32(tmem + O_COL + (t ^ 1) * D + lanes + c, q);
+            tmem_wait_ld32(q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = (f > 0.f ? o[i] * f : 0.f) + (fo > 0.f ? q[i] * fo : 0.f);
+          }
           uint4 w[4];
           if (direct) {
 #pragma unroll
@@ -822,7 +898,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.o_free[t]);
+      if (lane == 0) {  // O has been read: both halves', of a split piece, else this half's (both of its arrivals)
+        mbar_arrive(&bars.o_free[t]);
+        mbar_arrive(&bars.o_free[split ? t ^ 1 : t]);
+      }
     }
   }
   __syncthreads();
