@@ -495,8 +495,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (ok) {
               unsigned char* dst = smem + L::KV + ring.s * L::TILE;
               mbar_expect_tx(&bars.full[ring.s], L::TILE);
-#pragma unroll
-              for (int r = 0; r < NREG; ++r) tma_load_3d(dst + r * L::SLAB, map, &bars.full[ring.s], r * 64, row, slice);
+              tma_load_4d(dst, map, &bars.full[ring.s], 0, row, 0, slice);
               mine = ring;
               any = true;
             }

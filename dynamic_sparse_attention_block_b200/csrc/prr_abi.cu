@@ -222,11 +222,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 namespace prr {
 
-// 3-D map over a KV cache, box {64 channels, box_tokens (default bs) tokens, 1 slice}, 128-byte swizzle, zero
+// 3-D map over a KV cache, box {64 channels, bs tokens, 1 slice}, 128-byte swizzle, zero
 // fill outside the tensor.  Contiguous caches [B*Hkv][cap][d]: a slice is one
 // (sequence, KV head) pair.  Paged pools [pages*Hkv][bs][d]: a slice is one (page, KV
 // head) tile.
-bool make_kv_map(CUtensorMap* map, const void* base, const prr_dims* d, int box_tokens) {
+bool make_kv_map(CUtensorMap* map, const void* base, const prr_dims* d) {
   auto fn = encode_fn();
   if (!fn) return false;
   const bool paged = d->pages > 0;
@@ -234,9 +234,27 @@ bool make_kv_map(CUtensorMap* map, const void* base, const prr_dims* d, int box_
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d->d), rows,
                               static_cast<cuuint64_t>(paged ? d->pages : d->B) * d->Hkv};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d->d) * 2, static_cast<cuuint64_t>(d->d) * 2 * rows};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_tokens > 0 ? box_tokens : d->bs), 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(d->bs), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// The same caches in steps of 64 tokens, every channel in one copy: {64 channels, 64 tokens, d / 64, 1 slice}, so
+// that the tile lands as d / 64 slabs of 64 swizzled rows.
+bool make_kv_step_map(CUtensorMap* map, const void* base, const prr_dims* d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bool paged = d->pages > 0;
+  const cuuint64_t rows = static_cast<cuuint64_t>(paged ? d->bs : d->cap_tokens), row = static_cast<cuuint64_t>(d->d) * 2;
+  const cuuint64_t dims[4] = {64, rows, static_cast<cuuint64_t>(d->d / 64),
+                              static_cast<cuuint64_t>(paged ? d->pages : d->B) * d->Hkv};
+  const cuuint64_t strides[3] = {row, 128, row * rows};
+  const cuuint32_t box[4] = {64, 64, static_cast<cuuint32_t>(d->d / 64), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;

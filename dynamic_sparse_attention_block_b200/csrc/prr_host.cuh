@@ -21,7 +21,8 @@ inline prr_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PRR_OK 
 bool dims_ok(const prr_dims* d);
 DeviceInfo device_info();
 Params base_params(const prr_dims* d, void* ws, bool kv_units = false);
-bool make_kv_map(CUtensorMap* map, const void* base, const prr_dims* d, int box_tokens = 0);
+bool make_kv_map(CUtensorMap* map, const void* base, const prr_dims* d);
+bool make_kv_step_map(CUtensorMap* map, const void* base, const prr_dims* d);
 bool make_q_map(CUtensorMap* map, const void* base, int64_t stride, int32_t rows, const prr_dims* d);
 
 }  // namespace prr

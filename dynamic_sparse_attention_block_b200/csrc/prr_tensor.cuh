@@ -117,6 +117,16 @@ __device__ __forceinline__ void tmem_wait_ld32(float* r) {
                : "memory");
 }
 
+// 4-D tiled TMA load, completion on `bar`.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
+
 // One thread of the warp, the same one each time the whole warp asks.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;

@@ -30,7 +30,7 @@ prr_status attend(const prr_dims* d, Params& p, AttendArgs& a, void* ws, const S
   a.work = static_cast<unsigned char*>(ws) + L.attend;
   a.max_rows = max_rows;
   CUtensorMap qm = {}, km, vm;
-  if (!make_kv_map(&km, p.kc, d, 64) || !make_kv_map(&vm, p.vc, d, 64)) return PRR_ERR_CUDA;
+  if (!make_kv_step_map(&km, p.kc, d) || !make_kv_step_map(&vm, p.vc, d)) return PRR_ERR_CUDA;
   if (a.q_begin && !make_q_map(&qm, a.q, a.q_stride, a.rows, d)) return PRR_ERR_CUDA;
   return cuda_status(launch_attend(p, a, qm, km, vm, device_info().sms, stream));
 }
