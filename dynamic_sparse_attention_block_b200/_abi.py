@@ -339,49 +339,58 @@ def prr_decode_step_fused(dims, buffers: PrrStepBuffers, ws, step_parity: int, s
 
 
 # ----------------------------------------------------------------------------- around the decode step
-# Prompts and page tables.  Calls without a stream run on the current stream of the
-# workspace's device, and every call runs with that device current.
+# Prompts and page tables.  Every tensor of a call is on its workspace's device, which is
+# current while the call runs; calls without a stream run on that device's current stream.
+# (Written for few Python steps a call: these calls are short.)
 
-def _rows(t, heads: int, d: int, name: str):
-    """(address, elements between two rows) of packed rows [rows][heads][d] bf16."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != torch.bfloat16:
+def _at(t, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor on device `dev`."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("every tensor of a call must be a CUDA tensor on the workspace's device")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _vec(t, n: int, dev: int, name: str) -> int:
+    """Address of an int32 vector of at least n entries."""
+    if t.dtype is not torch.int32 or t.numel() < n:
+        raise ValueError(f"{name} must be int32 with {n} entries")
+    return _at(t, dev)
+
+
+def _rows(t, heads: int, d: int, dev: int, name: str):
+    """(address, rows, elements between two rows) of packed rows [rows][heads][d] bf16."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be bf16 [rows][{heads}][{d}]")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    rows, (stride, s1, s2) = t.shape[0], t.stride()
+    if t.get_device() != dev:
+        raise ValueError("every tensor of a call must be a CUDA tensor on the workspace's device")
+    rows, (stride, s1, s2) = shape[0], t.stride()
     if rows and (s2 != 1 or (heads > 1 and s1 != d) or (rows > 1 and stride < heads * d)):
         raise ValueError(f"the heads of one row of {name} must be contiguous, and its rows must not overlap")
-    return t.data_ptr(), stride if rows > 1 else heads * d
+    return t.data_ptr(), rows, stride if rows > 1 else heads * d
 
 
-def _vec(t, n: int, name: str, dtype=torch.int32):
-    """Address of a contiguous device vector of at least n entries."""
-    if t.dtype != dtype or t.numel() < n:
-        raise ValueError(f"{name} must be {dtype} with {n} entries")
-    return _ptr(t)
-
-
-def _serve(fn: str, ws, stream, *args) -> None:
-    """Call fn(*args, ws, ws_bytes, stream) with the workspace's device current; every tensor of the call is on it."""
-    index = ws.device.index
-    call = getattr(load(), fn)
-    if index == torch.cuda.current_device():
-        _check(call(*args, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), fn)
-    else:
-        with torch.cuda.device(index):
-            _check(call(*args, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), fn)
-
-
-def _same_device(ws, *tensors) -> None:
-    if any(t is not None and t.device != ws.device for t in tensors):
-        raise ValueError("every tensor of a call must be on the workspace's device")
-
-
-def _out_rows(out, lse, rows: int, c: PrrDims) -> None:
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != (rows, c.Hq, c.d):
+def _outs(out, lse, rows: int, c: PrrDims, dev: int):
+    """Addresses of the attention outputs out [rows][Hq][d] bf16 and lse [rows][Hq] fp32 (or None)."""
+    if out.dtype is not torch.bfloat16 or out.shape != (rows, c.Hq, c.d):
         raise ValueError(f"out must be bf16 [{rows}][{c.Hq}][{c.d}]")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (rows, c.Hq)):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, c.Hq)):
         raise ValueError(f"lse must be fp32 [{rows}][{c.Hq}]")
+    return _at(out, dev), _at(lse, dev)
+
+
+def _serve(fn: str, ws, dev: int, stream, *args) -> None:
+    """fn(*args, ws, ws_bytes, stream) with device `dev` current."""
+    if dev < 0:
+        raise ValueError("expected a CUDA workspace")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _serve(fn, ws, dev, stream, *args)
+    _check(getattr(_LIB or load(), fn)(*args, _at(ws, dev), ws.numel() * ws.element_size(), _stream(stream)), fn)
 
 
 def prr_serving_workspace_bytes(dims, max_rows: int) -> int:
@@ -396,61 +405,56 @@ def cache_buffers(k_cache=None, v_cache=None, block_table=None, page_refs=None, 
 
 
 def prr_append_prompt(dims, k_rows, v_rows, q_begin, seq_lens, k_cache, v_cache, summ, ws, stream=None) -> None:
-    c = _dims(dims)
-    kp, ks = _rows(k_rows, c.Hkv, c.d, "k_rows")
-    vp, vs = _rows(v_rows, c.Hkv, c.d, "v_rows")
-    if k_rows.shape[0] != v_rows.shape[0] or ks != vs:
+    c, dev = _dims(dims), ws.get_device()
+    kp, rows, ks = _rows(k_rows, c.Hkv, c.d, dev, "k_rows")
+    vp, vrows, vs = _rows(v_rows, c.Hkv, c.d, dev, "v_rows")
+    if rows != vrows or ks != vs:
         raise ValueError("k_rows and v_rows must have one shape and one row stride")
-    _same_device(ws, k_rows, v_rows, q_begin, seq_lens, k_cache, v_cache, summ)
-    _serve("prr_append_prompt", ws, stream, ctypes.byref(c), kp, vp, ks, _vec(q_begin, c.B + 1, "q_begin"),
-           k_rows.shape[0], _vec(seq_lens, c.B, "seq_lens"), _ptr(k_cache), _ptr(v_cache), _ptr(summ))
+    _serve("prr_append_prompt", ws, dev, stream, ctypes.byref(c), kp, vp, ks, _vec(q_begin, c.B + 1, dev, "q_begin"), rows,
+           _vec(seq_lens, c.B, dev, "seq_lens"), _at(k_cache, dev), _at(v_cache, dev), _at(summ, dev))
 
 
 def prr_attend_prompt(dims, q, q_begin, seq_lens, k_cache, v_cache, out, lse, ws, stream=None) -> None:
-    c = _dims(dims)
-    qp, qs = _rows(q, c.Hq, c.d, "q")
-    _out_rows(out, lse, q.shape[0], c)
-    _same_device(ws, q, q_begin, seq_lens, k_cache, v_cache, out, lse)
-    _serve("prr_attend_prompt", ws, stream, ctypes.byref(c), qp, qs, _vec(q_begin, c.B + 1, "q_begin"), q.shape[0],
-           _vec(seq_lens, c.B, "seq_lens"), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse))
+    c, dev = _dims(dims), ws.get_device()
+    qp, rows, qs = _rows(q, c.Hq, c.d, dev, "q")
+    op, lp = _outs(out, lse, rows, c, dev)
+    _serve("prr_attend_prompt", ws, dev, stream, ctypes.byref(c), qp, qs, _vec(q_begin, c.B + 1, dev, "q_begin"), rows,
+           _vec(seq_lens, c.B, dev, "seq_lens"), _at(k_cache, dev), _at(v_cache, dev), op, lp)
 
 
 def prr_attend_shared(dims, q, members, group_begin, shared_blocks, seq_lens, k_cache, v_cache, out, lse, ws,
                       stream=None) -> None:
-    c = _dims(dims)
-    qp, qs = _rows(q, c.Hq, c.d, "q")
-    if q.shape[0] != c.B:
+    c, dev = _dims(dims), ws.get_device()
+    qp, rows, qs = _rows(q, c.Hq, c.d, dev, "q")
+    if rows != c.B:
         raise ValueError(f"q must hold one row for each of the {c.B} sequences")
-    _out_rows(out, lse, c.B, c)
-    _same_device(ws, q, members, group_begin, shared_blocks, seq_lens, k_cache, v_cache, out, lse)
+    op, lp = _outs(out, lse, rows, c, dev)
     groups = shared_blocks.numel()
-    _serve("prr_attend_shared", ws, stream, ctypes.byref(c), qp, qs, _vec(members, 0, "members"), members.numel(),
-           _vec(group_begin, groups + 1, "group_begin"), _vec(shared_blocks, 0, "shared_blocks"), groups,
-           _vec(seq_lens, c.B, "seq_lens"), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse))
+    _serve("prr_attend_shared", ws, dev, stream, ctypes.byref(c), qp, qs, _vec(members, 0, dev, "members"), members.numel(),
+           _vec(group_begin, groups + 1, dev, "group_begin"), _vec(shared_blocks, 0, dev, "shared_blocks"), groups,
+           _vec(seq_lens, c.B, dev, "seq_lens"), _at(k_cache, dev), _at(v_cache, dev), op, lp)
 
 
 def prr_cache_reserve(dims, want_lens, cache: PrrCacheBuffers, ws, stream=None) -> None:
-    c = _dims(dims)
-    _same_device(ws, want_lens)
-    _serve("prr_cache_reserve", ws, stream, ctypes.byref(c), _vec(want_lens, c.B, "want_lens"), ctypes.byref(cache))
+    c, dev = _dims(dims), ws.get_device()
+    _serve("prr_cache_reserve", ws, dev, stream, ctypes.byref(c), _vec(want_lens, c.B, dev, "want_lens"), ctypes.byref(cache))
 
 
 def prr_cache_fork(dims, parents, children, cache: PrrCacheBuffers, ws, stream=None) -> None:
-    c = _dims(dims)
-    _same_device(ws, parents, children)
+    c, dev = _dims(dims), ws.get_device()
     n = children.numel()
-    _serve("prr_cache_fork", ws, stream, ctypes.byref(c), _vec(parents, n, "parents"), _vec(children, n, "children"), n,
-           ctypes.byref(cache))
+    if parents.numel() != n:
+        raise ValueError("one parent for each child")
+    _serve("prr_cache_fork", ws, dev, stream, ctypes.byref(c), _vec(parents, n, dev, "parents"),
+           _vec(children, n, dev, "children"), n, ctypes.byref(cache))
 
 
 def prr_cache_release(dims, seqs, cache: PrrCacheBuffers, ws, stream=None) -> None:
-    c = _dims(dims)
-    _same_device(ws, seqs)
-    _serve("prr_cache_release", ws, stream, ctypes.byref(c), _vec(seqs, 0, "seqs"), seqs.numel(), ctypes.byref(cache))
+    c, dev = _dims(dims), ws.get_device()
+    _serve("prr_cache_release", ws, dev, stream, ctypes.byref(c), _vec(seqs, 0, dev, "seqs"), seqs.numel(), ctypes.byref(cache))
 
 
 def prr_cache_compact(dims, cache: PrrCacheBuffers, remap, n_live, ws, stream=None) -> None:
-    c = _dims(dims)
-    _same_device(ws, remap, n_live)
-    _serve("prr_cache_compact", ws, stream, ctypes.byref(c), ctypes.byref(cache), _vec(remap, c.pages, "remap"),
-           _vec(n_live, 1, "n_live"))
+    c, dev = _dims(dims), ws.get_device()
+    _serve("prr_cache_compact", ws, dev, stream, ctypes.byref(c), ctypes.byref(cache), _vec(remap, c.pages, dev, "remap"),
+           _vec(n_live, 1, dev, "n_live"))

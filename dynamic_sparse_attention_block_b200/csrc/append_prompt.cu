@@ -19,8 +19,7 @@ __device__ __forceinline__ long long first_slot(const int* q_begin, int b, int b
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) append_prompt_kernel(const __grid_constant__ Params p,
-                                                            const __grid_constant__ AppendArgs a) {
+__device__ __forceinline__ void append_block(const Params& p, const AppendArgs& a) {
   constexpr int C = D / 8;     // 16-byte column chunks per row
   constexpr int RG = 128 / C;  // rows in flight
   __shared__ uint4 red_lo[RG][C];
@@ -39,7 +38,7 @@ __global__ void __launch_bounds__(128) append_prompt_kernel(const __grid_constan
   int r0, r1;
   if (!packed_range(a.q_begin, b, a.rows, &r0, &r1, p.status, tell) || r0 == r1 || j < 0) return;
   const int n0 = a.seq_lens[b];
-  if (n0 < 0 || n0 > p.cap - (r1 - r0)) return;  // advance_kernel says so
+  if (n0 < 0 || n0 > p.cap - (r1 - r0)) return;  // reported where the lengths advance
   const int n1 = n0 + (r1 - r0);
   const long long blk = n0 / p.bs + static_cast<long long>(j);
   const long long t0 = blk * p.bs;
@@ -96,26 +95,35 @@ __global__ void __launch_bounds__(128) append_prompt_kernel(const __grid_constan
   *dst = *reinterpret_cast<uint4*>(acc);
 }
 
-// seq_lens[b] += rows of b, once every block of the rows is written.
-__global__ void advance_kernel(const __grid_constant__ Params p, const __grid_constant__ AppendArgs a) {
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= p.B) return;
-  int r0, r1;
-  if (!packed_range(a.q_begin, b, a.rows, &r0, &r1, p.status, true) || r0 == r1) return;
-  const int n0 = a.seq_lens[b];
-  if (n0 < 0 || n0 > p.cap - (r1 - r0)) report(p.status, kDevBadSeqLen);
-  else a.seq_lens[b] = n0 + (r1 - r0);
+// One CTA per (touched block, head); the CTA that ends last advances the lengths, which the others read.
+template <int D>
+__global__ void __launch_bounds__(128) append_prompt_kernel(const __grid_constant__ Params p,
+                                                            const __grid_constant__ AppendArgs a) {
+  append_block<D>(p, a);
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned* ticket = reinterpret_cast<unsigned*>(p.status) + kTicketWord;
+    last = atom_add_acq_rel(ticket, 1u) == gridDim.x * gridDim.y - 1;
+    if (last) *ticket = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    int r0, r1;
+    if (!packed_range(a.q_begin, b, a.rows, &r0, &r1, p.status, true) || r0 == r1) continue;
+    const int n0 = a.seq_lens[b];
+    if (n0 < 0 || n0 > p.cap - (r1 - r0)) report(p.status, kDevBadSeqLen);
+    else a.seq_lens[b] = n0 + (r1 - r0);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_append_prompt(const Params& p, const AppendArgs& a, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.rows / p.bs + 2ll * p.B + 1), p.Hkv);
-  const cudaError_t e = p.d == 128
-      ? launch_kernel(append_prompt_kernel<128>, grid, dim3(128), 0, s, 0, p, a)
-      : launch_kernel(append_prompt_kernel<64>, grid, dim3(128), 0, s, 0, p, a);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(advance_kernel, dim3((p.B + 127) / 128), dim3(128), 0, s, 0, p, a);
+  return p.d == 128 ? launch_kernel(append_prompt_kernel<128>, grid, dim3(128), 0, s, 0, p, a)
+                    : launch_kernel(append_prompt_kernel<64>, grid, dim3(128), 0, s, 0, p, a);
 }
 
 }  // namespace prr

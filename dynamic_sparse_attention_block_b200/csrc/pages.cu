@@ -311,29 +311,29 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
   }
 }
 
-__global__ void __launch_bounds__(256) compact_copy_kernel(const __grid_constant__ Params p,
-                                                           const __grid_constant__ PageArgs a) {
-  const PageWork w = page_work(a.work, p.B, p.pages);
-  const size_t page = static_cast<size_t>(p.Hkv) * p.bs * p.d;
-  const int moves = w.count[0];
-  for (int i = blockIdx.x; i < moves; i += gridDim.x) {
-    const int src = w.movers[i], dst = w.list[i];
-    copy16(a.kc + dst * page, a.kc + src * page, page * 2, 0, 1);
-    copy16(a.vc + dst * page, a.vc + src * page, page * 2, 0, 1);
-  }
-}
+constexpr int kCompactCopyCtas = 1184, kCompactTableCtas = 148;
 
-__global__ void __launch_bounds__(256) compact_table_kernel(const __grid_constant__ Params p,
-                                                            const __grid_constant__ PageArgs a, const int* remap) {
+// The pages that move, and in the last CTAs the table entries and counts that follow them.
+__global__ void __launch_bounds__(256) compact_move_kernel(const __grid_constant__ Params p,
+                                                           const __grid_constant__ PageArgs a, const int* remap) {
   const PageWork w = page_work(a.work, p.B, p.pages);
-  const size_t n = static_cast<size_t>(p.B) * p.maxnb, step = static_cast<size_t>(gridDim.x) * blockDim.x;
-  const size_t t0 = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int moves = w.count[0];
+  if (blockIdx.x < kCompactCopyCtas) {
+    const size_t page = static_cast<size_t>(p.Hkv) * p.bs * p.d;
+    for (int i = blockIdx.x; i < moves; i += kCompactCopyCtas) {
+      const int src = w.movers[i], dst = w.list[i];
+      copy16(a.kc + dst * page, a.kc + src * page, page * 2, 0, 1);
+      copy16(a.vc + dst * page, a.vc + src * page, page * 2, 0, 1);
+    }
+    return;
+  }
+  const size_t n = static_cast<size_t>(p.B) * p.maxnb, step = static_cast<size_t>(kCompactTableCtas) * blockDim.x;
+  const size_t t0 = static_cast<size_t>(blockIdx.x - kCompactCopyCtas) * blockDim.x + threadIdx.x;
   for (size_t i = t0; i < n; i += step) {
     const int pg = a.table[i];
     if (pg >= 0 && pg < p.pages && remap[pg] >= 0) a.table[i] = remap[pg];
     else if (pg != -1) report(p.status, kDevBadRange);
   }
-  const int moves = w.count[0];
   for (size_t i = t0; i < static_cast<size_t>(moves); i += step) {
     const int src = w.movers[i], dst = w.list[i];
     a.refs[dst] = a.refs[src];
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(256) compact_table_kernel(const __grid_constan
 
 }  // namespace
 
-size_t page_work_words(const Params& p) { return 2 * static_cast<size_t>(p.pages) + 5 * static_cast<size_t>(p.B) + 4; }
+size_t page_work_words(int B, int pages) { return 2 * static_cast<size_t>(pages) + 5 * static_cast<size_t>(B) + 4; }
 
 cudaError_t launch_cache_reserve(const Params& p, const PageArgs& a, const int* want, cudaStream_t s) {
   return launch_kernel(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, s, 0, p, a, want);
@@ -364,9 +364,9 @@ cudaError_t launch_cache_release(const Params& p, const PageArgs& a, const int* 
 
 cudaError_t launch_cache_compact(const Params& p, const PageArgs& a, int* remap, int* n_live, cudaStream_t s) {
   cudaError_t e = launch_kernel(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, 0, p, a, remap, n_live);
-  if (e == cudaSuccess) e = launch_kernel(compact_copy_kernel, dim3(1184), dim3(256), 0, s, 0, p, a);
-  if (e == cudaSuccess) e = launch_kernel(compact_table_kernel, dim3(256), dim3(256), 0, s, 0, p, a,
-                                          static_cast<const int*>(remap));
+  if (e == cudaSuccess)
+    e = launch_kernel(compact_move_kernel, dim3(kCompactCopyCtas + kCompactTableCtas), dim3(256), 0, s, 0, p, a,
+                      static_cast<const int*>(remap));
   return e;
 }
 

@@ -52,6 +52,8 @@ struct AttendArgs {
   int max_rows;
 };
 
+constexpr int kTicketWord = 32;  // int32 word of the workspace: CTAs of a launch that are done; 0 between launches
+
 constexpr int kMaxAttendCtas = 160;  // the workspace holds partials for so many
 
 struct PageArgs {
@@ -70,7 +72,7 @@ struct PageArgs {
   int* work;        // page bookkeeping of the workspace
 };
 
-size_t page_work_words(const Params& p);
+size_t page_work_words(int B, int pages);
 size_t attend_tiles(int B, int max_rows, int G);
 size_t attend_work_bytes(int B, int Hq, int G, int d, int max_rows);
 

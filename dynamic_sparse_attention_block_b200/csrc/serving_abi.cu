@@ -1,5 +1,7 @@
 // serving_abi.cu -- host side of the calls around the decode step: argument and shape
 // rules, the serving workspace, launches.
+#include <cstring>
+
 #include "prr_host.cuh"
 #include "prr_serving.cuh"
 
@@ -9,10 +11,9 @@ namespace {
 
 ServeLayout serve_layout(const prr_dims* d, int32_t max_rows) {
   ServeLayout L = {};
-  const Params p = base_params(d, nullptr, true);
-  size_t off = 256;  // status word
+  size_t off = 256;  // status word, and behind it (kTicketWord) a ticket
   L.pages = off;
-  off = align256(off + 4 * page_work_words(p));
+  off = align256(off + 4 * page_work_words(d->B, d->pages));
   L.attend = off;
   off = align256(off + attend_work_bytes(d->B, d->Hq, d->Hq / d->Hkv, d->d, max_rows));
   L.total = off;
@@ -35,8 +36,26 @@ prr_status attend(const prr_dims* d, Params& p, AttendArgs& a, void* ws, const S
   return cuda_status(launch_attend(p, a, qm, km, vm, device_info().sms, stream));
 }
 
+// The kernel parameters that these calls read.
 Params serve_params(const prr_dims* d, void* ws, const ServeLayout& L) {
-  Params p = base_params(d, nullptr, true);
+  Params p;
+  std::memset(&p, 0, sizeof p);
+  p.B = d->B;
+  p.Hq = d->Hq;
+  p.Hkv = d->Hkv;
+  p.G = d->Hq / d->Hkv;
+  p.upb = d->Hkv;
+  p.kv_div = 1;
+  p.units = d->B * d->Hkv;
+  p.d = d->d;
+  p.bs = d->bs;
+  p.cap = d->cap_tokens;
+  p.K = d->K;
+  p.P = d->P;
+  p.maxnb = (d->cap_tokens + d->bs - 1) / d->bs;
+  p.pages = d->pages;
+  p.table = d->block_table;
+  p.scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634074);
   p.status = reinterpret_cast<int*>(static_cast<unsigned char*>(ws) + L.status);
   return p;
 }
