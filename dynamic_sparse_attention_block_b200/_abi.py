@@ -390,7 +390,8 @@ def _serve(fn: str, ws, dev: int, stream, *args) -> None:
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _serve(fn, ws, dev, stream, *args)
-    _check(getattr(_LIB or load(), fn)(*args, _at(ws, dev), ws.numel() * ws.element_size(), _stream(stream)), fn)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    _check(getattr(_LIB or load(), fn)(*args, _at(ws, dev), ws.numel() * ws.element_size(), st), fn)
 
 
 def prr_serving_workspace_bytes(dims, max_rows: int) -> int:
