@@ -140,8 +140,8 @@ prr_status prr_attend_shared(const prr_dims* dims, const uint16_t* q, int64_t q_
                              const uint16_t* v_cache, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                              cudaStream_t stream) {
   if (!dims_ok(dims) || !stride_ok(q_stride, dims->Hq, dims->d)) return PRR_ERR_SHAPE;
-  if (n_members < 0 || n_members > dims->B || n_groups < 0 || n_groups > n_members) return PRR_ERR_SHAPE;
-  if (n_groups == 0) return PRR_OK;
+  if (n_members < 0 || n_members > dims->B || n_groups < 0 || n_groups > dims->B) return PRR_ERR_SHAPE;
+  if (n_groups == 0 || n_members == 0) return PRR_OK;
   if (!q || !members || !group_begin || !shared_blocks || !seq_lens || !k_cache || !v_cache || !out || !ws)
     return PRR_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PRR_ERR_INVALID_ARG;

@@ -457,8 +457,8 @@ prr_status prr_attend_prompt(const prr_dims* dims, const uint16_t* q, int64_t q_
 
 /* Attention of one query per sequence, q [B][Hq][d] bf16, over ALL of its tokens, for a
  * batch in groups that share a prefix: group g is members[group_begin[g] ..
- * group_begin[g+1]) (device int32; group_begin [n_groups+1] ascending from 0,
- * n_members <= B), and the first shared_blocks[g] blocks are the same for all of its
+ * group_begin[g+1]) (device int32; group_begin [n_groups+1] ascending from 0, n_members
+ * and n_groups at most B), and the first shared_blocks[g] blocks are the same for all of its
  * members.  They are read once for the whole group, through its first member's rows of
  * the cache (its part of the block table), and must be full: shared_blocks[g]*bs <=
  * seq_lens of every member.  0 shares nothing.  out [B][Hq][d] bf16, lse [B][Hq] fp32

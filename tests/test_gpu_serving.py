@@ -246,6 +246,7 @@ def _shared(c, members, gb, sb, q=None, ws=None):
     ([7, 1, 128, 64, False, [0], [[1, 0, 500, 1300]]]),
     ([8, 8, 64, 64, True, [33], [[4] * 260]]),
     ([4, 1, 64, 64, True, [300], [[0]]]),
+    ([12, 4, 128, 64, True, [5, 9, 3], [[], [7, 70], []]]),  # groups of no one
 ])
 def test_attend_shared(Hq, Hkv, d, bs, paged, prefix, own):
     lens, gb, share = [], [0], []
@@ -528,6 +529,102 @@ def test_release_reports_a_count_that_did_not_know_of_a_row():
     prr.prr_cache_release(dims, _i32([0, 1]), bufs, ws)
     assert prr.prr_get_device_status(ws) == 5
     assert refs.tolist() == [0, 0] and lens.tolist() == [0, 0] and bool((table == -1).all())
+
+
+@pytest.mark.parametrize("selector,n_rep", [("per_head", 0), ("representative", 3)])
+def test_fork_and_release_carry_the_state_of_every_selector(selector, n_rep):
+    B, Hq, Hkv, d, bs, maxnb, P, pages = 3, 4, 2, 64, 64, 4, 5, 12
+    S = Hq if selector == "per_head" else Hkv
+    table, refs, lens = _i32([[3, 7, 1, -1], [-1] * 4, [-1] * 4]), _i32(np.zeros(pages)), _i32([150, 0, 0])
+    refs[[3, 7, 1]] = 1
+    rep = torch.randint(0, bs, (B, Hkv, maxnb, max(n_rep, 1)), dtype=torch.uint8, device=DEV)
+    dims = prr.Dims(B=B, Hq=Hq, Hkv=Hkv, d=d, bs=bs, cap_tokens=maxnb * bs, K=2, P=P, pages=pages, selector=selector,
+                    n_rep=n_rep, block_table=table.data_ptr(), rep_offsets=rep.data_ptr() if n_rep else None)
+    kc = torch.randn(pages, Hkv, bs, d, device=DEV).bfloat16()
+    vc = torch.randn(pages, Hkv, bs, d, device=DEV).bfloat16()
+    ema = torch.rand(B, S, maxnb, dtype=torch.float64, device=DEV)
+    pred = torch.randint(0, 9, (B, S, P), dtype=torch.int32, device=DEV)
+    rep0, ema0, pred0 = rep.clone(), ema.clone(), pred.clone()
+    bufs = prr.cache_buffers(kc, vc, table, refs, lens, None, ema, pred, rep if n_rep else None)
+    ws = torch.zeros(prr.prr_serving_workspace_bytes(dims, 1), dtype=torch.uint8, device=DEV)
+    prr.prr_cache_fork(dims, _i32([0]), _i32([2]), bufs, ws)
+    assert prr.prr_get_device_status(ws) == 0
+    assert table.tolist()[2] == [3, 7, 0, -1] and lens.tolist() == [150, 0, 150]
+    assert torch.equal(kc[0], kc[1]) and torch.equal(vc[0], vc[1])
+    assert torch.equal(ema[2, :, :3], ema0[0, :, :3]) and not ema[2, :, 3].any() and torch.equal(pred[2], pred0[0])
+    if n_rep:
+        assert torch.equal(rep[2, :, :3], rep0[0, :, :3]) and torch.equal(rep[2, :, 3], rep0[2, :, 3])
+    prr.prr_cache_release(dims, _i32([2]), bufs, ws)
+    assert refs.tolist()[:8] == [0, 1, 0, 1, 0, 0, 0, 1] and not ema[2].any()
+    assert bool((pred[2] == _i32(np.arange(P))).all())
+    assert torch.equal(ema[:2], ema0[:2]) and torch.equal(pred[:2], pred0[:2])
+
+
+def test_caches_past_two_to_the_31_elements():
+    """Offsets into K and V of more than 2^31 elements: appended, attended and compacted at the far end."""
+    Hkv, d, bs, n = 8, 128, 128, 300
+    pages = (1 << 31) // (Hkv * bs * d) + 6
+    kc = torch.zeros(pages, Hkv, bs, d, dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    used = [pages - 1, pages - 3, pages - 2]
+    table, refs = _i32([used]), _i32(np.zeros(pages))
+    refs[used] = 1
+    dims = prr.Dims(B=1, Hq=8, Hkv=Hkv, d=d, bs=bs, cap_tokens=3 * bs, K=1, P=0, pages=pages, block_table=table.data_ptr())
+    lens = _i32([0])
+    ws = torch.zeros(prr.prr_serving_workspace_bytes(dims, n), dtype=torch.uint8, device=DEV)
+    c = Case(8, Hkv, d, bs, [n], False)
+    qb = _i32([0, n])
+    prr.prr_append_prompt(dims, c.k[0].transpose(0, 1).contiguous(), c.v[0].transpose(0, 1).contiguous(), qb, lens, kc, vc,
+                          None, ws)
+    q = c.randn(n, 8, d)
+    for _ in range(2):
+        out, lse = torch.zeros_like(q), torch.zeros(n, 8, device=DEV)
+        prr.prr_attend_prompt(dims, q, qb, lens, kc, vc, out, lse, ws)
+        c.check(q, out, lse, _some((i, 0, i + 1) for i in range(n)))
+        remap, live = torch.zeros(pages, dtype=torch.int32, device=DEV), _i32([0])
+        prr.prr_cache_compact(dims, prr.cache_buffers(kc, vc, table, refs, lens), remap, live, ws)
+        assert int(live) == 3 and table.tolist() == [[2, 0, 1]] and refs.tolist()[:4] == [1, 1, 1, 0]
+    assert prr.prr_get_device_status(ws) == 0
+
+
+def test_serving_calls_captured_and_replayed():
+    """One graph of a turn -- rows appended and attended, a fork, the shared attention, a release -- replayed twice."""
+    B, Hq, Hkv, d, bs, n = 3, 8, 2, 64, 64, 200
+    dims = prr.Dims(B=B, Hq=Hq, Hkv=Hkv, d=d, bs=bs, cap_tokens=512, K=2, P=0, pages=20)
+    dec = prr.PRRDecoder(dims, empty=True)
+    dec.reserve([n, 0, 0])
+    c = Case(Hq, Hkv, d, bs, [n], False)
+    k, v, q = (x.transpose(0, 1).contiguous() for x in (c.k[0], c.v[0], c.randn(Hq, n, d)))
+    qb, kids, pars, mem, gb, sb = _i32([0, n, n, n]), _i32([1, 2]), _i32([0, 0]), _i32([2, 0, 1]), _i32([0, 3]), _i32([3])
+    q1 = c.randn(B, Hq, d)
+    ws = torch.zeros(prr.prr_serving_workspace_bytes(dec.dims, n), dtype=torch.uint8, device=DEV)
+    out, lse, out1, lse1 = (torch.zeros(s, dtype=t, device=DEV) for s, t in (
+        ((n, Hq, d), torch.bfloat16), ((n, Hq), torch.float32), ((B, Hq, d), torch.bfloat16), ((B, Hq), torch.float32)))
+    lens0, bufs = torch.zeros_like(dec.seq_lens), dec.cache_buffers()
+
+    def turn():
+        dec.seq_lens.copy_(lens0)
+        prr.prr_append_prompt(dec.dims, k, v, qb, dec.seq_lens, dec.k_cache, dec.v_cache, dec.summ, ws)
+        prr.prr_attend_prompt(dec.dims, q, qb, dec.seq_lens, dec.k_cache, dec.v_cache, out, lse, ws)
+        prr.prr_cache_fork(dec.dims, pars, kids, bufs, ws)
+        prr.prr_attend_shared(dec.dims, q1, mem, gb, sb, dec.seq_lens, dec.k_cache, dec.v_cache, out1, lse1, ws)
+        prr.prr_cache_release(dec.dims, kids, bufs, ws)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        turn()
+    for _ in range(2):
+        for t in (out, lse, out1, lse1):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(q, out, lse, _some((i, 0, i + 1) for i in range(n)))
+        for b in range(B):
+            o, l, tol, ltol = c.exact(q1[b], 0, n)
+            assert bool(((out1[b].double() - o).abs() <= tol).all()) and bool(((lse1[b].double() - l).abs() <= ltol).all())
+        assert dec.seq_lens.tolist() == [n, 0, 0] and int((dec.page_refs > 0).sum()) == 4
+    assert prr.prr_get_device_status(ws) == 0
 
 
 # ----------------------------------------------------------------------------- together
