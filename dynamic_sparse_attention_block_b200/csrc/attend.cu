@@ -8,21 +8,29 @@
 // Tiles.  A tile is up to 256 rows that read the same tokens of one KV head: the G query
 // heads of its group times up to 2 * floor(128/G) packed tokens of one prompt, or the G heads of
 // that many members of a group (over the shared prefix) or of one sequence (over its own
-// tokens).  It is attended in blocks of 128 tokens; a tile's weight is its number of
-// blocks.  The plan kernel numbers all (head, tile, block) units and cuts them into
-// equal runs, one per CTA, wherever the cuts fall -- so prompts, single tokens, long
-// prefixes and ragged batches all fill the machine evenly.  A tile cut between CTAs (and every
-// tile of a batch in groups) leaves fp32 partials (m, sum, O) that combine kernels merge.
+// tokens).  Its work is counted in blocks of 128 tokens.  The plan kernel numbers all (head, tile,
+// block) units and cuts them into equal runs, one per CTA, wherever the cuts fall -- so prompts,
+// single tokens, long prefixes and ragged batches all fill the machine evenly.  A tile cut
+// between CTAs (and every tile of a batch in groups) leaves fp32 partials (m, sum, O) that the
+// combine kernels merge.
 //
-// A CTA (one per SM) runs, per tile piece: one thread that issues the TMA copies of K and
-// V blocks through a ring of stages; one that issues the products; two warps that bring
-// the next piece's rows of Q as soon as the last product has read the present ones; and two groups of
-// 128 threads, one per 128 rows, each thread owning one row.  For rows t in {0, 1}:
-//   S_t = Q_t K^T (tensor memory), softmax group t turns S_t into P_t = 2^(s' - m) in place,
-//   O_t += P_t V (tensor memory), with S of one half and the softmax of the other overlapping.
-// P is rounded to bf16 (the product's operand type): half a step, 2^-8 of each weight at most; its sum,
-// m and O stay fp32.  m only moves when a row's maximum grew by more than 2^8: until then weights up
-// to 256 are exact in range, and O needs no rescaling.
+// A CTA (one per SM) works on a piece of a tile, in steps of 64 tokens:
+//  - one thread per half (128 rows) issues its products on the tensor cores: S = Q K^T into tensor
+//    memory, O += P V with P read from there.  S is asked for one step ahead (two buffers of 64
+//    columns; with O, 2 x d columns, tensor memory is full);
+//  - a warp copies K and V by TMA into a ring of stages, another brings the next piece's Q;
+//  - two groups of 128 threads, one thread to a row, turn S into P = 2^(s' - m) in place.
+// A tile of up to 128 rows is split: both halves take its rows, each every other step, and merge
+// through tensor memory at the end.
+//
+// P is rounded to bf16 (the products' operand type): half a step, 2^-8 of each weight at most;
+// its sum, m and O stay fp32, and the result is rounded once.  m only moves when a row's
+// maximum grew by more than 2^8: until then weights up to 256 stay in range, and O needs no rescaling.
+//
+// Measured (B200, 32/8 heads, d 128): a 32K prompt in 8.3 ms, 1060 TFLOP/s or 64% of a measured
+// matrix product; bound by the softmax's latency and the products (tensor pipe 70% busy; Q K^T with
+// 64 columns is limited by shared memory, 48 clocks where 128 columns take 64).  One step of 128 tokens
+// without S ahead: 900 TFLOP/s.  64 queries of 64/8 heads on four prefixes of 128K: 490 us, 4.6 TB/s or 70% of a measured copy.
 #include "prr_serving.cuh"
 #include "prr_tensor.cuh"
 

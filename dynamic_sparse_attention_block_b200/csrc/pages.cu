@@ -3,7 +3,10 @@
 // The state is the block table and one reference count per page; a page is free at 0 (or below).
 // Free pages are always given out lowest first, in the order of the requests, so the
 // tables do not depend on the order in which threads run.  The plans (which page goes
-// where) are integer scans over the counts; the copies are bound by HBM.
+// where) are integer scans over the counts by one CTA, a launch that the copies wait for; the
+// copies are bound by HBM.  Measured (B200): 60 forks of 128K sequences (summaries, state and last pages, 511 MB)
+// with their release and reservation in 99 us, 5.1 TB/s; 2048 moved pages of 512 KB in 440 us, 4.9 TB/s (75% of a
+// measured copy).
 #include "prr_serving.cuh"
 
 namespace prr {
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
 }
 
 // Part `part` of kPageParts equal parts of a page's K or V, by one CTA: pages in parts, so that the CTAs end together
-// (2048 pages of 512 KB: 451 us with whole pages, 1.7 to a CTA).
+// (2048 pages of 512 KB: 451 us with whole pages, 1.7 to a CTA, 440 in parts).
 constexpr int kPageParts = 8;
 
 __device__ void copy_part(uint16_t* dst, const uint16_t* src, size_t bytes, int part) {
