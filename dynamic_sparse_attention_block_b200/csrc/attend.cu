@@ -27,10 +27,11 @@
 // its sum, m and O stay fp32, and the result is rounded once.  m only moves when a row's
 // maximum grew by more than 2^8: until then weights up to 256 stay in range, and O needs no rescaling.
 //
-// Measured (B200, 32/8 heads, d 128): a 32K prompt in 8.3 ms, 1060 TFLOP/s or 64% of a measured
-// matrix product; bound by the softmax's latency and the products (tensor pipe 70% busy; Q K^T with
+// Measured (B200, 32/8 heads, d 128): a 32K prompt in 8.3 to 8.6 ms, 1020 to 1060 TFLOP/s or 62 to 64%
+// of a measured matrix product; bound by the softmax's latency and the products (tensor pipe 70% busy; Q K^T with
 // 64 columns is limited by shared memory, 48 clocks where 128 columns take 64).  One step of 128 tokens
-// without S ahead: 900 TFLOP/s.  64 queries of 64/8 heads on four prefixes of 128K: 490 us, 4.6 TB/s or 70% of a measured copy.
+// without S ahead: 900 TFLOP/s.  64 queries of 64/8 heads on four prefixes of 128K: 490 to 520 us,
+// 4.3 to 4.6 TB/s or 66 to 70% of a measured copy.
 #include "prr_serving.cuh"
 #include "prr_tensor.cuh"
 
@@ -173,7 +174,7 @@ __device__ bool group_entry(const Params& p, const AttendArgs& a, int i, Entry* 
   }
   e->seq = a.members[i];
   e->first = a.members[e->g0];
-  if (e->seq < 0 || e->seq >= p.B || e->first < 0 || e->first >= p.B) {
+  if (e->seq < 0 || e->seq >= p.B || (sb > 0 && (e->first < 0 || e->first >= p.B))) {
     report(p.status, kDevBadRange);
     return false;
   }
@@ -867,13 +868,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           }
         }
         // Each thread has one row; 64 bytes of the warp's rows at a time go through shared memory, so
-        // that four threads store 64 consecutive bytes of a row.
+        // that four threads store 64 consecutive bytes of a row; few rows go straight out (a batch of 64 sequences
+        // with four prefixes of 128K: 513 us through shared memory, 503 us so).
         char* own = row < 0 ? nullptr : direct ? reinterpret_cast<char*>(a.out + at * D) : reinterpret_cast<char*>(part + 4);
         char* to[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           to[i] = reinterpret_cast<char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(own), 8 * i + lane / 4));
+        const bool few = ntok * G <= 16;
         auto store64 = [&](const uint4 (&w)[4], int offset) {
+          if (few) {
+            if (own)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(own + offset + i * 16) = w[i];
+            return;
+          }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = w[i];

@@ -333,6 +333,8 @@ class PRRDecoder:
             if need == 0:
                 raise ValueError(f"unsupported number of rows {rows}")
             if self.serve_ws is None or self.serve_ws.numel() < need:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the serving workspace has to grow: make a call of this size before the capture")
                 status = 0 if self.serve_ws is None else self.serve_ws[:4].clone()
                 self.serve_ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
                 self.serve_ws[:4] = status

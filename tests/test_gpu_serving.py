@@ -268,6 +268,20 @@ def test_attend_shared(Hq, Hkv, d, bs, paged, prefix, own):
     assert prr.prr_get_device_status(ws) == 0
 
 
+def test_a_batch_of_three_thousand_single_tokens():
+    """More sequences than the plan keeps on chip, through both attention calls; most CTAs have many pieces."""
+    B = 3000
+    lens = [int(x) for x in np.random.RandomState(0).randint(1, 200, B)]
+    c = Case(4, 2, 64, 64, lens, True)
+    q, qb, out, lse, ws = _prompt(c, [1] * B, tail=0)
+    rows = _some(((b, b, lens[b]) for b in range(B)), 40)
+    c.check(q, out, lse, rows)
+    _, out2, lse2, ws2 = _shared(c, np.random.RandomState(1).permutation(B), [0, B], [0], q=q)
+    c.check(q, out2, lse2, rows)
+    assert (out.float() - out2.float()).abs().max() < 0.05 and bool((lse - lse2).abs().max() < 1e-4)
+    assert prr.prr_get_device_status(ws) == 0 and prr.prr_get_device_status(ws2) == 0
+
+
 def test_attend_shared_reads_the_prefix_through_its_first_member():
     """The other members' copies of a shared prefix are not read: they may hold anything."""
     c = Case(4, 1, 64, 64, [200, 210, 150], False, share=[(0, 1, 128), (0, 2, 128)])
@@ -298,6 +312,7 @@ def test_attend_shared_equals_itself_in_a_graph_and_with_a_sequence_listed_twice
     ([0, 9, 2], [0, 3], [1], None, 5, [0, 2]), ([-1, 1, 2], [0, 3], [1], None, 5, []),
     ([0, 1, 2], [0, 3], [3], None, 5, [0, 1]), ([0, 1, 2], [0, 3], [-1], None, 5, []),
     ([0, 1, 2], [0, 4], [1], None, 5, []), ([0, 1, 2], [0, 1, 3], [1, 9], None, 5, [0]),
+    ([-1, 1, 2], [0, 3], [0], None, 5, [1, 2]),  # nothing is read through the first member
     ([0, 1, 2], [0, 3], [1], [200, -1, 130], 1, [0, 2]), ([0, 1, 2], [0, 3], [1], [200, 1 << 29, 130], 1, [0, 2]),
 ])
 def test_attend_shared_bad_entries_are_skipped(members, gb, sb, lens, code, good):
