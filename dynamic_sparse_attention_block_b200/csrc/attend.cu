@@ -596,6 +596,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         // the previous piece's O has been read
         ok = ok && thread_wait(&bars.o_free[t], fph, abort, p.status);
         fph ^= 1;
+        // without a step here the piece could end before that wait, and its phase pass unseen: the softmax threads
+        // wait for this
+        if (ok && mine == 0) mbar_arrive(&bars.o_full[t]);
         for (int i = 0; ok && i < rounds; ++i) {
           const bool more = i + 2 < mine;
           const uint32_t buf = used & 1;
@@ -818,10 +821,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[t][buf]);
       }
-      if (n > 0) {
-        ok = ok && role_wait(&bars.o_full[t], oph, abort, p.status);
-        oph ^= 1;
-      }
+      ok = ok && role_wait(&bars.o_full[t], oph, abort, p.status);
+      oph ^= 1;
       if (!ok) break;
       tc_fence_after();
       unsigned char* box = smem + L::OUT + warp * 2048;

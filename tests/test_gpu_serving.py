@@ -247,6 +247,7 @@ def _shared(c, members, gb, sb, q=None, ws=None):
     ([8, 8, 64, 64, True, [33], [[4] * 260]]),
     ([4, 1, 64, 64, True, [300], [[0]]]),
     ([12, 4, 128, 64, True, [5, 9, 3], [[], [7, 70], []]]),  # groups of no one
+    ([7, 1, 128, 64, True, [19] * 4, [[1, 2, 3, 4] * 3 + [1]] * 4]),  # a CTA whose only piece is one step of few rows
 ])
 def test_attend_shared(Hq, Hkv, d, bs, paged, prefix, own):
     lens, gb, share = [], [0], []
