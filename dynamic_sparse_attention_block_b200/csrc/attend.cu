@@ -28,7 +28,7 @@
 // maximum grew by more than 2^8: until then weights up to 256 stay in range, and O needs no rescaling.
 //
 // Measured (B200, 32/8 heads, d 128): a 32K prompt in 8.3 to 8.6 ms, 1020 to 1060 TFLOP/s or 62 to 64%
-// of a measured matrix product; bound by the softmax's latency and the products (tensor pipe 70% busy; Q K^T with
+// of a measured matrix product; bound by the softmax's latency and the products (tensor pipe 75% busy; Q K^T with
 // 64 columns is limited by shared memory, 48 clocks where 128 columns take 64).  One step of 128 tokens
 // without S ahead: 900 TFLOP/s.  64 queries of 64/8 heads on four prefixes of 128K: 490 to 520 us,
 // 4.3 to 4.6 TB/s or 66 to 70% of a measured copy.
@@ -43,7 +43,7 @@ constexpr int kBlock = 128;         // tokens per unit of work
 constexpr int kStep = 64;           // tokens per product: two steps of S in tensor memory, one ahead
 constexpr float kGrow = 8.0f;       // log2 of the growth that moves the reference m
 constexpr int kPlanThreads = 1024;
-constexpr int kAttendThreads = 384;  // 2 x 128 softmax threads; warps for products, copies, Q (2)
+constexpr int kAttendThreads = 384;  // 2 x 128 softmax threads; two warps for products, one for copies, one for Q
 
 __host__ __device__ constexpr int sub_tokens(int G) { return kBlock / G; }  // packed tokens per 128 rows
 
@@ -75,7 +75,7 @@ struct PlanHead {
 
 struct Plan {
   PlanHead* head;
-  Start* start;        // [kMaxAttendCtas + 1]
+  Start* start;        // [kMaxAttendCtas]
   long long* prefix;   // [tiles + 1] units before each tile
   Tile* tile;
   int* row;            // [B] batch in groups: the sequence of each entry, -1: skipped
