@@ -348,7 +348,7 @@ __device__ inline FinishOut select_finish(const Params& p, int u, int nb, unsign
       ++active_local;
       atomicOr(&bm_pred[pv >> 5], 1u << (pv & 31));
       if (j > 0 && spred[j - 1] >= pv) report(p.status, kDevBadPred);
-    } else if (pv != -1) {
+    } else if (pv != -1 && pv != j) {  // (slot j naming block j: the zero state's list, which waits for the block)
       report(p.status, kDevBadPred);
     }
   }

@@ -105,7 +105,7 @@ class PRRDecoder:
         self.trace = None      # optional per-item timeline of fused launches (enable_trace)
         self.stats = None      # optional step counters (enable_stats)
         self.serve_ws = None   # workspace of the calls around the step (_serving)
-        if empty and P > 0:    # what the zero state predicts
+        if empty and P > 0:    # what the zero state predicts, of the blocks that the sequence then has
             self.pred_buf.copy_(torch.arange(P, dtype=torch.int32, device=dev))
 
     def _count_refs(self, pages: int) -> torch.Tensor:

@@ -90,7 +90,7 @@ typedef enum {
 /* Device status codes (the value prr_get_device_status stores in *code). */
 #define PRR_DEV_OK 0
 #define PRR_DEV_BAD_SEQ_LEN 1  /* seq_lens[b] < 1 or > cap_tokens (that sequence is skipped) */
-#define PRR_DEV_BAD_PRED 2     /* predicted list entry out of range or not ascending */
+#define PRR_DEV_BAD_PRED 2     /* predicted list entry out of range (neither a block, nor -1, nor pred[j] = j) or not ascending */
 #define PRR_DEV_BAD_MISSED 3   /* missed list entry out of range */
 #define PRR_DEV_WAIT_TIMEOUT 4 /* a bounded wait for a TMA copy gave up */
 #define PRR_DEV_BAD_RANGE 5    /* summary update range outside [0, cap_tokens] or longer than max_range_tokens, or a block-table entry outside [0, pages) */
@@ -279,6 +279,8 @@ prr_status prr_update_summaries(const prr_dims* dims, const uint16_t* k_cache,
  * sum_c max(q_hc*min_bc, q_hc*max_bc); sel = the min(K, nb) best blocks under (score
  * desc, block asc), written ascending; missed = sel \ pred ascending, n_missed its
  * size; keep[j] = (pred[j] in sel).  A predicted slot is active when 0 <= pred[j] < nb.
+ * An inactive one holds -1, or its own index: 0..P-1 is what the zero state predicts
+ * before the sequence has a length, and at any length its first min(P, nb) entries count.
  * PRR abstract: the true selected set; method summary: repair only the missed blocks. */
 prr_status prr_select_topk(const prr_dims* dims, const uint16_t* q, const uint16_t* summ,
                            const int32_t* seq_lens, const int32_t* pred, int32_t* sel,
@@ -514,8 +516,8 @@ prr_status prr_cache_fork(const prr_dims* dims, const int32_t* parents, const in
 
 /* Release the sequences seqs[0..n) (device int32, n <= B): their pages lose one reference
  * each, their table rows become -1, their lengths 0, and where the buffers are given
- * their EMA state 0 and their prediction that of the zero state (blocks 0 .. P-1), so
- * that the slot can take another sequence.  A second entry for a sequence does nothing;
+ * their EMA state 0 and their prediction that of the zero state (blocks 0 .. P-1, of
+ * which a step takes those that the next sequence has), so that the slot can take another sequence.  A second entry for a sequence does nothing;
  * an index outside [0, B), a table entry outside the pool and a page whose count is 0
  * already set PRR_DEV_BAD_RANGE.  Needs block_table, page_refs and seq_lens. */
 prr_status prr_cache_release(const prr_dims* dims, const int32_t* seqs, int32_t n,
