@@ -27,6 +27,9 @@
 // its sum, m and O stay fp32, and the result is rounded once.  m only moves when a row's
 // maximum grew by more than 2^8: until then weights up to 256 stay in range, and O needs no rescaling.
 //
+// A maximum passes over NaN, a sum does not: partials of no token are told by sum = 0, and a row of scores that are
+// not finite carries its NaN through every merge (m is -infinity for both).
+//
 // Measured (B200, 32/8 heads, d 128): a 32K prompt in 8.3 to 8.6 ms, 1020 to 1060 TFLOP/s or 62 to 64%
 // of a measured matrix product; bound by the softmax's latency and the products (tensor pipe 75% busy; Q K^T with
 // 64 columns is limited by shared memory, 48 clocks where 128 columns take 64).  One step of 128 tokens
@@ -841,8 +844,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(there);
         const float both = fmaxf(m, o.x);
-        f = m == -INFINITY ? 0.f : exp2_fast(m - both);
-        fo = o.x == -INFINITY ? 0.f : exp2_fast(o.x - both);
+        f = sum == 0.f ? 0.f : exp2_fast(m - both);
+        fo = o.y == 0.f ? 0.f : exp2_fast(o.x - both);
         m = both;
         sum = sum * f + o.y * fo;
         ok = role_wait(here, 1, abort, p.status);  // the other half has read the box
@@ -851,7 +854,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       if (work) {
         const int hq = x.head * G + g;
         const bool direct = a.q_begin && x.whole;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = 1.f / sum;  // (a row of a whole tile has tokens: 0 / 0 where every score is -infinity)
         const size_t at = static_cast<size_t>(row < 0 ? 0 : row) * p.Hq + hq;
         // partial rows: of the CTA (a tile's later pieces; of a prompt also its first), or of the batch
         const int prow0 = (split ? 0 : t * 128) + tid;
@@ -906,7 +909,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             tmem_ld32(tmem + O_COL + (t ^ 1) * D + lanes + c, q);
             tmem_wait_ld32(q);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = (f > 0.f ? o[i] * f : 0.f) + (fo > 0.f ? q[i] * fo : 0.f);
+            for (int i = 0; i < 32; ++i) o[i] = (f != 0.f ? o[i] * f : 0.f) + (fo != 0.f ? q[i] * fo : 0.f);
           }
           uint4 w[4];
           if (direct) {
@@ -958,6 +961,7 @@ __device__ void merge_few(const Plan& plan, const AttendArgs& a, int n, size_t a
 #pragma unroll
   for (int i = 0; i < kFewRows; ++i) {
     rm[i] = -INFINITY;
+    rs[i] = 0.f;
     if (i < n) {
       const float* r = plan.part + row_of(i) * (D + 4);
       rm[i] = r[0];
@@ -973,17 +977,17 @@ __device__ void merge_few(const Plan& plan, const AttendArgs& a, int n, size_t a
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
 #pragma unroll
   for (int i = 0; i < kFewRows; ++i) {
-    if (rm[i] == -INFINITY) continue;  // nothing there: the rest of the row may hold anything
+    if (rs[i] == 0.f) continue;  // nothing there: the rest of the row may hold anything
     const float f = exp2f(rm[i] - m);
     sum += rs[i] * f;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] += ro[i][c] * f;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = n == 0 ? 0.f : 1.f / sum;  // no piece: a sequence without tokens
 #pragma unroll
   for (int c = 0; c < C; c += 2)
     reinterpret_cast<uint32_t*>(a.out + at * D + lane * C)[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
-  if (a.lse && lane == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse && lane == 0) a.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Many rows: one CTA, its warps taking every kMergeWarps-th, with the loads of four rows under way at a time.
@@ -1001,6 +1005,7 @@ __device__ void merge_many(const Plan& plan, const AttendArgs& a, int n, size_t 
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u * kMergeWarps;
       rm[u] = -INFINITY;
+      rs[u] = 0.f;
       if (i < n) {
         const float* r = plan.part + row_of(i) * (D + 4);
         rm[u] = r[0];
@@ -1010,15 +1015,14 @@ __device__ void merge_many(const Plan& plan, const AttendArgs& a, int n, size_t 
       }
     }
     const float m1 = fmaxf(m, fmaxf(fmaxf(rm[0], rm[1]), fmaxf(rm[2], rm[3])));
-    if (m1 == -INFINITY) continue;
-    const float f = exp2f(m - m1);
+    const float f = m == m1 ? 1.f : exp2f(m - m1);  // (the same infinity: nothing to rescale)
     m = m1;
     sum *= f;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] *= f;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (rm[u] == -INFINITY) continue;  // nothing there: the rest of the row may hold anything
+      if (rs[u] == 0.f) continue;  // nothing there: the rest of the row may hold anything
       const float g = exp2f(rm[u] - m);
       sum += rs[u] * g;
 #pragma unroll
@@ -1039,14 +1043,14 @@ __device__ void merge_many(const Plan& plan, const AttendArgs& a, int n, size_t 
   float x = 0.f, y = 0.f;
   sum = 0.f;
   for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - m);
+    const float f = s_sum[w] == 0.f ? 0.f : exp2f(s_m[w] - m);
     sum += s_sum[w] * f;
     x += s_acc[w][2 * threadIdx.x] * f;
     y += s_acc[w][2 * threadIdx.x + 1] * f;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = 1.f / sum;  // (there is a piece, so there are tokens)
   reinterpret_cast<uint32_t*>(a.out + at * D)[threadIdx.x] = pack_bf16(x * inv, y * inv);
-  if (a.lse && threadIdx.x == 0) a.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (a.lse && threadIdx.x == 0) a.lse[at] = (m + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Packed prompts: CTA column c merges the tile that was cut first at the start of CTA c's run.

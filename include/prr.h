@@ -451,7 +451,8 @@ prr_status prr_append_prompt(const prr_dims* dims, const uint16_t* k_rows, const
  * written); only the sequences' rows are written.  A sequence with more rows than
  * tokens, or a length outside [1, cap_tokens], sets PRR_DEV_BAD_SEQ_LEN and is skipped.
  * Cache rows at or past seq_lens[b] may hold anything (NaN included); those below it are
- * finite. */
+ * finite.  A row and head of q that is not finite, or whose products with the keys all
+ * overflow, gets NaN in out (an lse that is not finite) and changes no other result. */
 prr_status prr_attend_prompt(const prr_dims* dims, const uint16_t* q, int64_t q_stride,
                              const int32_t* q_begin, int32_t rows, const int32_t* seq_lens,
                              const uint16_t* k_cache, const uint16_t* v_cache, uint16_t* out,

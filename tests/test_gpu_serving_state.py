@@ -83,3 +83,69 @@ def test_a_prediction_of_blocks_that_are_not_there_is_still_reported(entries):
     dec.pred.copy_(_i32([[entries]]))
     _step(dec, "fused", q[-1:])
     assert dec.device_status() == 2
+
+
+# ----------------------------------------------------------------------------- queries that are not finite
+
+def _spoil(q, rows):
+    """Every third of the rows gets one head that holds a NaN or an infinity; returns {row: head}."""
+    bad = {}
+    for i, r in enumerate(rows[::3]):
+        h = (5 * i) % q.shape[1]
+        q[r, h, i % q.shape[2]] = (NAN, INF, -INF)[i % 3]
+        bad[r] = h
+    return bad
+
+
+def _check_spoiled(c, q, bad, out, lse, rows):
+    clean = q.clone()
+    for r, h in bad.items():
+        clean[r, h] = 0
+    o, l = out.clone(), lse.clone()
+    for r, b, n in rows:
+        if r in bad:  # one head of the row: NaN in every channel; the others as they are
+            h = bad[r]
+            assert bool(out[r, h].isnan().all()), (r, b, n, out[r, h][:4])
+            assert not bool(lse[r, h].isfinite()), (r, b, n)
+            if bool(q[r, h].isnan().any()):
+                assert bool(lse[r, h].isnan()), (r, b, n)
+            eo, el, _, _ = c.exact(clean[r], b, n)
+            o[r, h], l[r, h] = eo[h], el[h].float()
+    c.check(clean, o, l, rows)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,bs,paged,new,old", [
+    (32, 8, 128, 64, True, [300], [0]),         # whole and cut tiles of more than 128 rows
+    (4, 1, 64, 64, False, [3], [20000]),        # few rows, cut between all CTAs
+    (8, 2, 128, 128, True, [1] * 400, [70] * 400),  # one piece a sequence, of few rows
+    (6, 2, 64, 64, True, [40, 1, 130], [500, 0, 9000]),
+])
+def test_attend_prompt_queries_that_are_not_finite(Hq, Hkv, d, bs, paged, new, old):
+    c = Case(Hq, Hkv, d, bs, [a + b for a, b in zip(new, old)], paged)
+    q = c.randn(sum(new), Hq, d)
+    at = np.concatenate([[0], np.cumsum(new)])
+    rows = _some([(int(at[b]) + i, b, old[b] + i + 1) for b in range(c.B) for i in range(new[b])], 60)
+    bad = _spoil(q, [r for r, _, _ in rows])
+    q, _, out, lse, ws = _prompt(c, new, q=q)
+    _check_spoiled(c, q, bad, out, lse, rows)
+    assert prr.prr_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("prefix,own", [([20, 0], [[5, 600, 0, 129], [1, 77, 0]]), ([300], [[1] * 70]), ([0], [[9000]])])
+def test_attend_shared_queries_that_are_not_finite(prefix, own):
+    bs, lens, gb, share = 64, [], [0], []
+    for pb, tails in zip(prefix, own):
+        first = len(lens)
+        lens += [pb * bs + t for t in tails]
+        share += [(first, b, pb * bs) for b in range(first + 1, len(lens))]
+        gb.append(len(lens))
+    c = Case(8, 2, 128, bs, lens, True, share=share)
+    q = c.randn(c.B, 8, 128)
+    bad = _spoil(q, list(range(c.B)))
+    q[[b for b in range(c.B) if lens[b] == 0]] = NAN
+    q, out, lse, ws = _shared(c, list(range(c.B)), gb, prefix, q=q)
+    _check_spoiled(c, q, bad, out, lse, [(b, b, lens[b]) for b in range(c.B) if lens[b]])
+    for b in range(c.B):
+        if lens[b] == 0:  # attends nothing, whatever its query
+            assert bool((out[b] == 0).all()) and bool((lse[b] == -math.inf).all())
+    assert prr.prr_get_device_status(ws) == 0
