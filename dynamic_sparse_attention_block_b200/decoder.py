@@ -243,18 +243,22 @@ class PRRDecoder:
     def checkpoint(self) -> dict:
         """Host copies of the state a decode step carries to the next one: the caches,
         sequence lengths, block summaries, EMA state and the current prediction Pred_t
-        (and the block table of a paged cache).  The workspace holds nothing that
-        outlives a step, so it is not part of the state."""
+        (and the block table of a paged cache, and the representatives' offsets, which
+        fork() copies).  The workspace holds nothing that outlives a step, so it is not
+        part of the state."""
         self.select_stream.synchronize()
         ck = {"k_cache": self.k_cache.cpu(), "v_cache": self.v_cache.cpu(), "seq_lens": self.seq_lens.cpu(),
               "summ": self.summ.cpu(), "ema": self.ema.cpu(), "pred": self.pred.cpu()}
         if self.block_table is not None:
             ck["block_table"] = self.block_table.cpu()
+        if self.rep_offsets is not None:
+            ck["rep_offsets"] = self.rep_offsets.cpu()
         return ck
 
     def restore(self, ck: dict) -> None:
         """Load a checkpoint() into this decoder (same dims): the next step continues
-        exactly where the checkpointed decoder stopped."""
+        exactly where the checkpointed decoder stopped.  (A checkpoint of before it held
+        the representatives' offsets leaves this decoder's as they are.)"""
         self._after_caller(self.select_stream)
         with torch.cuda.stream(self.select_stream):
             for name in ("k_cache", "v_cache", "seq_lens", "summ", "ema"):
@@ -263,6 +267,8 @@ class PRRDecoder:
                 self.block_table.copy_(ck["block_table"])
                 self.table_host = ck["block_table"].numpy().copy()
                 self.page_refs.copy_(self._count_refs(self.dims.pages))
+            if self.rep_offsets is not None and "rep_offsets" in ck:
+                self.rep_offsets.copy_(ck["rep_offsets"])
             self.parity, self.fused_parity = 0, 0
             self.pred_buf[0].copy_(ck["pred"])
             _abi.prr_workspace_init(self.ws, self.select_stream)

@@ -149,3 +149,39 @@ def test_attend_shared_queries_that_are_not_finite(prefix, own):
         if lens[b] == 0:  # attends nothing, whatever its query
             assert bool((out[b] == 0).all()) and bool((lse[b] == -math.inf).all())
     assert prr.prr_get_device_status(ws) == 0
+
+
+# ----------------------------------------------------------------------------- checkpoints, the caller's tensors
+
+def _representative(seed=0):
+    B, Hq, Hkv, d, bs, n_rep = 2, 4, 2, 64, 64, 2
+    g = torch.Generator().manual_seed(seed)
+    dims = prr.Dims(B=B, Hq=Hq, Hkv=Hkv, d=d, bs=bs, cap_tokens=1024, K=3, P=2, pages=40, selector="representative",
+                    n_rep=n_rep)
+    rep = torch.randint(0, bs, (B, Hkv, dims.maxnb, n_rep), generator=g, dtype=torch.uint8)
+    return dims, rep
+
+
+def test_a_checkpoint_holds_the_representatives_that_a_fork_copied():
+    n = 900
+    dims, rep = _representative()
+    k, v, q = _tokens(n, 2, 2, 4, d=64)
+    kn, vn, qn = _tokens(2, 2, 2, 4, d=64, seed=3)
+    dec = prr.PRRDecoder(dims, rep_offsets=rep, empty=True)
+    dec.reserve([n, 0])
+    dec.append_prompt(k, v, [0, n, n])
+    before = dec.checkpoint()
+    dec.fork([0], [1])
+    dec.reserve([n + 2] * 2)
+    ck = dec.checkpoint()
+    other = prr.PRRDecoder(dims, rep_offsets=rep, empty=True)
+    other.restore(ck)
+    for x in (dec, other):
+        _step(x, "fused", qn, kn, vn)
+    assert torch.equal(other.rep_offsets, dec.rep_offsets)
+    assert torch.equal(other.sel, dec.sel) and torch.equal(other.out, dec.out)
+    dec.restore(before)  # back across the fork
+    assert torch.equal(dec.rep_offsets.cpu(), rep)
+    del ck["rep_offsets"]  # of a decoder that never forked: the offsets it was built with are its own
+    other.restore(ck)
+    assert other.device_status() == 0
