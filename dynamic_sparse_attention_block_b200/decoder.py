@@ -35,7 +35,8 @@ class PRRDecoder:
         block j of sequence b in page b*maxnb + j; with `empty` no sequence holds a page,
         and reserve() hands them out.  The representative-key selector
         takes `rep_offsets` (uint8 [B][Hkv][maxnb][n_rep], offsets of each block's
-        representative tokens inside the block)."""
+        representative tokens inside the block).  Both are copied: reserve(), fork(),
+        release() and compact() write the decoder's own."""
         if not torch.cuda.is_available():
             raise RuntimeError("PRRDecoder needs a CUDA device")
         _abi.load()
@@ -53,7 +54,7 @@ class PRRDecoder:
                 block_table = torch.full((B, maxnb), -1, dtype=torch.int32)
             elif block_table is None:
                 block_table = torch.arange(B * maxnb, dtype=torch.int32).view(B, maxnb)
-            self.block_table = block_table.to(device=dev, dtype=torch.int32).contiguous()
+            self.block_table = block_table.to(device=dev, dtype=torch.int32, copy=True).contiguous()
             self.table_host = self.block_table.cpu().numpy()
             self.page_refs = self._count_refs(dims.pages).to(dev)
             dims = dataclasses.replace(dims, block_table=self.block_table.data_ptr())
@@ -64,7 +65,7 @@ class PRRDecoder:
         if dims.selector == "representative":
             if rep_offsets is None or tuple(rep_offsets.shape) != (B, Hkv, maxnb, dims.n_rep):
                 raise ValueError("the representative selector needs rep_offsets [B][Hkv][maxnb][n_rep]")
-            self.rep_offsets = rep_offsets.to(device=dev, dtype=torch.uint8).contiguous()
+            self.rep_offsets = rep_offsets.to(device=dev, dtype=torch.uint8, copy=True).contiguous()
             dims = dataclasses.replace(dims, rep_offsets=self.rep_offsets.data_ptr())
         self.dims = dims
         self.v_cache = torch.zeros_like(self.k_cache)

@@ -185,3 +185,20 @@ def test_a_checkpoint_holds_the_representatives_that_a_fork_copied():
     del ck["rep_offsets"]  # of a decoder that never forked: the offsets it was built with are its own
     other.restore(ck)
     assert other.device_status() == 0
+
+
+def test_the_callers_table_and_offsets_are_not_written():
+    dims, rep = _representative(1)
+    table = torch.full((2, dims.maxnb), -1, dtype=torch.int32, device=DEV)
+    table[0, :3] = _i32([7, 1, 30])
+    rep = rep.to(DEV)
+    rep0, table0 = rep.clone(), table.clone()
+    dec = prr.PRRDecoder(dims, block_table=table, rep_offsets=rep)
+    dec.seq_lens.copy_(_i32([150, 0]))
+    dec.fork([0], [1])
+    dec.compact()
+    dec.reserve([150, 400])
+    dec.release([0])
+    assert dec.device_status() == 0 and not torch.equal(dec.block_table, table0)
+    assert torch.equal(dec.rep_offsets[1, :, :3], rep0[0, :, :3])
+    assert torch.equal(table, table0) and torch.equal(rep, rep0)
