@@ -134,7 +134,7 @@ static __device__ void count_tail(const Params& p, const FusedCtl& C) {
     if (atom_add_acq_rel(C.words + kCtlTail, 1u) + 1u == total && p.append_kv) {
       for (int b = 0; b < p.B; ++b) {
         const int n0 = p.seq_lens[b];
-        if (n0 >= 0 && n0 < p.cap) const_cast<int*>(p.seq_lens)[b] = n0 + 1;
+        if (n0 >= 0 && n0 < p.cap && !(n0 == 0 && idle_slot(p, b))) const_cast<int*>(p.seq_lens)[b] = n0 + 1;
       }
     }
   }

@@ -51,11 +51,20 @@ cudaError_t launch_kernel_early(void (*kernel)(KArgs...), dim3 grid, dim3 block,
 // (kernel, device).  Kept out of the launch path so that launches stay capturable.
 cudaError_t allow_max_smem(const void* kernel);
 
+// A slot of a paged cache that holds nothing: sequence b, of length 0, has no page for its first block.  Steps and
+// appends pass over it.
+__device__ __forceinline__ bool idle_slot(const Params& p, int b) {
+  return p.table && p.table[static_cast<size_t>(b) * p.maxnb] < 0;
+}
+
 // Tokens n of sequence b this launch works on -- seq_lens[b], plus the token the fused
-// step appends itself -- if n lies in [1, cap], otherwise 0 (and the status word says so).
+// step appends itself -- if n lies in [1, cap], otherwise 0 (and, but for a slot that holds nothing, the status
+// word says so).
 __device__ __forceinline__ int checked_len(const Params& p, int b, const Grp& g) {
-  const int n = p.seq_lens[b] + p.append_kv;
-  if (n < 1 || n > p.cap) {
+  const int len = p.seq_lens[b], n = len + p.append_kv;
+  if (len < 1 || len > p.cap - p.append_kv) {
+    if (len == 0 && idle_slot(p, b)) return 0;
+    if (n >= 1 && n <= p.cap) return n;  // a sequence's first token
     if (g.tid == 0) report(p.status, kDevBadSeqLen);
     return 0;
   }

@@ -10,7 +10,7 @@ namespace prr {
 // Device status codes written (first error wins) into the workspace status word.
 enum : int {
   kDevOk = 0,
-  kDevBadSeqLen = 1,      // seq_lens[b] < 1 or > cap_tokens
+  kDevBadSeqLen = 1,      // seq_lens[b] < 1 (but for idle slots) or > cap_tokens
   kDevBadPred = 2,         // predicted list not strictly ascending / out of range
   kDevBadMissed = 3,       // missed list entry out of range
   kDevWaitTimeout = 4,     // a bounded mbarrier wait gave up

@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(128) update_summaries_kernel(const __grid_cons
     end = p.tok_end[b];
   } else {
     end = p.seq_lens[b];
+    if (end == 0 && idle_slot(p, b)) return;
     begin = end - 1;
   }
   if (begin < 0 || end > p.cap || begin > end) {
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(128) append_kv_kernel(const Params p, const ui
                                                         uint16_t* vc, int* seq_lens) {
   const int b = blockIdx.x;
   const int pos = seq_lens[b];
+  if (pos == 0 && idle_slot(p, b)) return;
   bool ok = pos >= 0 && pos < p.cap;
   if (ok) {
     constexpr int C = D / 8;

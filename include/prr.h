@@ -89,7 +89,7 @@ typedef enum {
 
 /* Device status codes (the value prr_get_device_status stores in *code). */
 #define PRR_DEV_OK 0
-#define PRR_DEV_BAD_SEQ_LEN 1  /* seq_lens[b] < 1 or > cap_tokens (that sequence is skipped) */
+#define PRR_DEV_BAD_SEQ_LEN 1  /* seq_lens[b] < 1 or > cap_tokens (that sequence is skipped); not for an idle slot, see prr_dims::pages */
 #define PRR_DEV_BAD_PRED 2     /* predicted list entry out of range (neither a block, nor -1, nor pred[j] = j) or not ascending */
 #define PRR_DEV_BAD_MISSED 3   /* missed list entry out of range */
 #define PRR_DEV_WAIT_TIMEOUT 4 /* a bounded wait for a TMA copy gave up */
@@ -137,7 +137,10 @@ typedef struct {
    * KV head, and block_table (device int32 [B][maxnb]) maps block j of sequence b to its
    * page.  cap_tokens stays the per-sequence capacity.  Only entries of blocks below a
    * sequence's length are read; an entry outside [0, pages) sets PRR_DEV_BAD_RANGE and
-   * that block is not read. */
+   * that block is not read.  A sequence of length 0 whose first entry is negative is an
+   * idle slot (as prr_cache_release leaves one): appends and steps pass over it and
+   * report nothing; a step selects nothing for it, predicts -1 and writes zeros to out
+   * and -infinity to lse. */
   int32_t pages;
   const int32_t* block_table;
   /* PRR_SELECT_REPRESENTATIVE only (the other selectors ignore them): n_rep (1..16)
@@ -254,7 +257,8 @@ prr_status prr_get_device_status(const void* ws, int32_t* code);
 
 /* Write one new token per (sequence, KV head): k_new/v_new [B][Hkv][d] go to position
  * seq_lens[b] of the caches, then seq_lens[b] is incremented (a full cache leaves
- * seq_lens unchanged and sets PRR_DEV_BAD_SEQ_LEN).  The pages take the decode loop's
+ * seq_lens unchanged and sets PRR_DEV_BAD_SEQ_LEN; idle slots, see prr_dims::pages, are
+ * passed over).  The pages take the decode loop's
  * one-token-per-step cache growth as given; this is that step, not part of PRR. */
 prr_status prr_append_kv(const prr_dims* dims, const uint16_t* k_new, const uint16_t* v_new,
                          int32_t* seq_lens, uint16_t* k_cache, uint16_t* v_cache, void* ws,

@@ -202,3 +202,73 @@ def test_the_callers_table_and_offsets_are_not_written():
     assert dec.device_status() == 0 and not torch.equal(dec.block_table, table0)
     assert torch.equal(dec.rep_offsets[1, :, :3], rep0[0, :, :3])
     assert torch.equal(table, table0) and torch.equal(rep, rep0)
+
+
+# ----------------------------------------------------------------------------- slots without tokens, tokens without pages
+
+@pytest.mark.parametrize("mode", ["fused", "host", "streams"])
+@pytest.mark.parametrize("selector", ["group_sum", "per_head"])
+def test_steps_pass_over_slots_that_hold_nothing(mode, selector):
+    """A batch with idle slots decodes as the others alone would; the idle ones can be filled and forked into after."""
+    Hq, Hkv, d, bs, n = 8, 2, 64, 64, 300
+    sizes = dict(Hq=Hq, Hkv=Hkv, d=d, bs=bs, cap_tokens=1024, K=3, P=3, selector=selector)
+    dec = prr.PRRDecoder(prr.Dims(B=4, pages=60, **sizes), empty=True)
+    one = prr.PRRDecoder(prr.Dims(B=1, **sizes))
+    k, v = _tokens(n, Hkv, Hkv, d=d)
+    dec.reserve([50, n + 8, 0, 0])
+    dec.append_prompt(torch.cat([k[:50], k]), torch.cat([v[:50], v]), [0, 50, 50 + n, 50 + n, 50 + n])
+    dec.release([0])  # slot 0 was used, slots 2 and 3 never were
+    one.prefill(k.transpose(0, 1)[None], v.transpose(0, 1)[None], n)
+    idle = [0, 2, 3]
+    for step in range(4):
+        q, kn, vn = _tokens(4, Hq, Hkv, Hkv, d=d, seed=10 + step)
+        token = (kn, vn) if step != 2 else (None, None)
+        _step(dec, mode, q, *token)
+        _step(one, mode, q[1:2], *(x if x is None else x[1:2] for x in token))
+        assert dec.device_status() == 0 and one.device_status() == 0, step
+        assert dec.seq_lens.tolist() == [0, int(one.seq_lens), 0, 0], step
+        assert bool((dec.out[idle] == 0).all()) and bool((dec.lse[idle] == -INF).all()), step
+        assert bool((dec.sel[idle] == -1).all()) and not bool(dec.n_missed[idle].any()) and not bool(dec.keep[idle].any())
+        assert not bool(dec.ema[idle].any()) and bool((dec.block_table[idle] == -1).all()), step
+        assert torch.equal(dec.sel[1], one.sel[0]) and torch.equal(dec.pred[1], one.pred[0]), step
+        assert (dec.out[1] - one.out[0]).abs().max() < 1e-5, step
+    now = int(one.seq_lens)
+    dec.fork([1], [2])
+    dec.reserve([n + 1, now + 1, now + 1, 0])
+    dec.append_prompt(k, v, [0, n, n, n, n])
+    q, kn, vn = _tokens(4, Hq, Hkv, Hkv, d=d, seed=20)
+    q[2], kn[2], vn[2] = q[1], kn[1], vn[1]
+    fresh = prr.PRRDecoder(prr.Dims(B=1, **sizes))
+    fresh.prefill(k.transpose(0, 1)[None], v.transpose(0, 1)[None], n)
+    _step(dec, mode, q, kn, vn)
+    _step(one, mode, q[1:2], kn[1:2], vn[1:2])
+    _step(fresh, mode, q[:1], kn[:1], vn[:1])
+    assert dec.device_status() == 0 and dec.seq_lens.tolist() == [n + 1, now + 1, now + 1, 0]
+    for b, x in ((0, fresh), (1, one), (2, one)):
+        assert torch.equal(dec.sel[b], x.sel[0]) and (dec.out[b] - x.out[0]).abs().max() < 1e-5, b
+    assert bool((dec.out[3] == 0).all()) and bool((dec.lse[3] == -INF).all())
+
+
+@pytest.mark.parametrize("mode", ["fused", "host", "streams"])
+def test_a_step_starts_an_empty_sequence_that_has_its_page(mode):
+    dec = prr.PRRDecoder(prr.Dims(B=3, Hq=4, Hkv=1, d=64, bs=64, cap_tokens=256, K=4, P=2, pages=9), empty=True)
+    dec.reserve([0, 1, 70])
+    q, k, v = _tokens(3, 4, 1, 1, d=64)
+    _step(dec, mode, q, k, v)
+    assert dec.device_status() == 0 and dec.seq_lens.tolist() == [0, 1, 1]
+    assert torch.equal(dec.out[1:], v[1:].float().expand(2, 4, 64)) and bool((dec.out[0] == 0).all())
+    assert torch.equal(dec.summ[1:, :, 0, 0], k[1:]) and torch.equal(dec.summ[1:, :, 0, 1], k[1:])
+
+
+def test_separate_calls_pass_over_an_empty_slot_and_report_an_empty_sequence_of_a_contiguous_cache():
+    dims = prr.Dims(B=2, Hq=4, Hkv=1, d=64, bs=64, cap_tokens=256, K=4, P=2, pages=9)
+    dec = prr.PRRDecoder(dims, empty=True)
+    dec.reserve([0, 5])
+    q, k, v = _tokens(2, 4, 1, 1, d=64)
+    dec.append(k, v)
+    prr.prr_update_summaries(dec.dims, dec.k_cache, None, None, dec.seq_lens, 1, dec.summ, dec.ws, dec.select_stream)
+    dec.select_stream.synchronize()
+    assert dec.device_status() == 0 and dec.seq_lens.tolist() == [0, 1] and torch.equal(dec.summ[1, 0, 0, 0], k[1, 0])
+    flat = prr.PRRDecoder(prr.Dims(B=2, Hq=4, Hkv=1, d=64, bs=64, cap_tokens=256, K=4, P=2))
+    _step(flat, "fused", q)
+    assert flat.device_status() == 1
