@@ -126,17 +126,21 @@ __device__ __forceinline__ void count_done(unsigned* counter) {
 // A merge or predictor update is done; the CTA that finishes the last one of the step
 // advances seq_lens when the launch appended the step's token (every item has read
 // seq_lens by then: each reads it as it starts, and all of them start before the last
-// merge can finish).
+// merge can finish).  A token whose block has no page was dropped, and does not count.
 static __device__ void count_tail(const Params& p, const FusedCtl& C) {
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  bool last = false;
+  if (lane == 0) {
     const unsigned total = static_cast<unsigned>(p.units) * (p.G + 1);
-    if (atom_add_acq_rel(C.words + kCtlTail, 1u) + 1u == total && p.append_kv) {
-      for (int b = 0; b < p.B; ++b) {
-        const int n0 = p.seq_lens[b];
-        if (n0 >= 0 && n0 < p.cap && !(n0 == 0 && idle_slot(p, b))) const_cast<int*>(p.seq_lens)[b] = n0 + 1;
-      }
-    }
+    last = atom_add_acq_rel(C.words + kCtlTail, 1u) + 1u == total && p.append_kv;
+  }
+  if (!__any_sync(0xFFFFFFFFu, last)) return;
+  for (int b = lane; b < p.B; b += 32) {  // (a lane each: with pages it takes two dependent loads)
+    const int n0 = p.seq_lens[b];
+    if (n0 < 0 || n0 >= p.cap || (n0 == 0 && idle_slot(p, b))) continue;
+    if (kv_row(p, b * p.Hkv, n0) >= 0) const_cast<int*>(p.seq_lens)[b] = n0 + 1;
   }
 }
 

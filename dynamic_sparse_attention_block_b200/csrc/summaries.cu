@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(128) append_kv_kernel(const Params p, const ui
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    if (ok) seq_lens[b] = pos + 1;
-    else report(p.status, kDevBadSeqLen);
+    if (!ok) report(p.status, kDevBadSeqLen);
+    else if (kv_row(p, b * p.Hkv, pos) >= 0) seq_lens[b] = pos + 1;  // else the token was dropped
   }
 }
 

@@ -180,7 +180,9 @@ typedef struct {
    * The step's new token [B][Hkv][d] bf16 (16-byte aligned).  The step then appends it
    * itself: it writes the rows at position seq_lens[b] of the caches, works on
    * seq_lens[b] + 1 tokens and advances seq_lens[b] when it is done (a full cache sets
-   * PRR_DEV_BAD_SEQ_LEN and skips that sequence).  prr_decode_step_fused does this
+   * PRR_DEV_BAD_SEQ_LEN and skips that sequence; a token whose block has no page sets
+   * PRR_DEV_BAD_RANGE and is dropped: seq_lens[b] stays, and the sequence's results of
+   * this step do not count).  prr_decode_step_fused does this
    * inside its one launch; prr_decode_step launches the append first. */
   const uint16_t* k_new;
   const uint16_t* v_new;
@@ -258,7 +260,8 @@ prr_status prr_get_device_status(const void* ws, int32_t* code);
 /* Write one new token per (sequence, KV head): k_new/v_new [B][Hkv][d] go to position
  * seq_lens[b] of the caches, then seq_lens[b] is incremented (a full cache leaves
  * seq_lens unchanged and sets PRR_DEV_BAD_SEQ_LEN; idle slots, see prr_dims::pages, are
- * passed over).  The pages take the decode loop's
+ * passed over; a token whose block has no page is dropped, sets PRR_DEV_BAD_RANGE and
+ * leaves seq_lens unchanged).  The pages take the decode loop's
  * one-token-per-step cache growth as given; this is that step, not part of PRR. */
 prr_status prr_append_kv(const prr_dims* dims, const uint16_t* k_new, const uint16_t* v_new,
                          int32_t* seq_lens, uint16_t* k_cache, uint16_t* v_cache, void* ws,

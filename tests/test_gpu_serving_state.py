@@ -272,3 +272,29 @@ def test_separate_calls_pass_over_an_empty_slot_and_report_an_empty_sequence_of_
     flat = prr.PRRDecoder(prr.Dims(B=2, Hq=4, Hkv=1, d=64, bs=64, cap_tokens=256, K=4, P=2))
     _step(flat, "fused", q)
     assert flat.device_status() == 1
+
+
+@pytest.mark.parametrize("mode", ["fused", "host", "streams"])
+@pytest.mark.parametrize("n,entry", [(64, -1), (128, 10 ** 6), (70, -1)])
+def test_a_token_without_a_page_is_dropped_and_can_be_given_again(mode, n, entry):
+    """Its sequence keeps its length, so that reserve() still sees the missing block and the next step appends there."""
+    dims = prr.Dims(B=2, Hq=4, Hkv=2, d=64, bs=64, cap_tokens=512, K=8, P=2, pages=12)
+    dec = prr.PRRDecoder(dims, empty=True)
+    k, v = _tokens(n, 2, 2, d=64)
+    dec.reserve([n, n + 2])
+    dec.append_prompt(torch.cat([k, k]), torch.cat([v, v]), [0, n, 2 * n])
+    page = int(dec.block_table[0, n // 64])
+    dec.block_table[0, n // 64] = entry
+    q, kn, vn = _tokens(2, 4, 2, 2, d=64, seed=2)
+    _step(dec, mode, q, kn, vn)
+    assert dec.device_status() == 5 and dec.seq_lens.tolist() == [n, n + 1]
+    prr.prr_workspace_init(dec.ws)
+    dec.block_table[0, n // 64] = page
+    dec.reserve([n + 1, n + 2])
+    q[1], kn[1], vn[1] = q[0], kn[0], vn[0]
+    _step(dec, mode, q, kn, vn)
+    assert dec.device_status() == 0 and dec.seq_lens.tolist() == [n + 1, n + 2]
+    kk, vv = (torch.cat([x, y[:1]]).double().repeat_interleave(2, 1) for x, y in ((k, kn), (v, vn)))
+    w = torch.softmax(torch.einsum("hd,nhd->hn", q[0].double(), kk) / 8, -1)
+    # weights in two bf16 parts (2^-16 of each), fp32 sums
+    assert (dec.out[0] - torch.einsum("hn,nhd->hd", w, vv)).abs().max() < 2.0 ** -13
