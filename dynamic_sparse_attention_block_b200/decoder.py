@@ -106,6 +106,8 @@ class PRRDecoder:
         self.trace = None      # optional per-item timeline of fused launches (enable_trace)
         self.stats = None      # optional step counters (enable_stats)
         self.serve_ws = None   # workspace of the calls around the step (_serving)
+        self.serve_captured = False  # a captured graph works in it
+        self.serve_kept = []   # earlier ones that captured graphs work in
         if empty and P > 0:    # what the zero state predicts, of the blocks that the sequence then has
             self.pred_buf.copy_(torch.arange(P, dtype=torch.int32, device=dev))
 
@@ -332,19 +334,25 @@ class PRRDecoder:
     @contextlib.contextmanager
     def _serving(self, rows: int = 1):
         """The serving workspace, large enough for `rows` packed rows (allocated when a
-        call first needs it, or more of it), with the step stream current."""
+        call first needs it, or more of it), with the step stream current.  One that a
+        captured graph works in is kept as long as the decoder, whatever comes after it."""
         cur = torch.cuda.current_stream(self.device)
         self._after_caller(self.select_stream)
         with torch.cuda.stream(self.select_stream):
             need = _abi.prr_serving_workspace_bytes(self.dims, max(rows, 1))
             if need == 0:
                 raise ValueError(f"unsupported number of rows {rows}")
+            capturing = torch.cuda.is_current_stream_capturing()
             if self.serve_ws is None or self.serve_ws.numel() < need:
-                if torch.cuda.is_current_stream_capturing():
+                if capturing:
                     raise RuntimeError("the serving workspace has to grow: make a call of this size before the capture")
-                status = 0 if self.serve_ws is None else self.serve_ws[:4].clone()
-                self.serve_ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
-                self.serve_ws[:4] = status
+                ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
+                if self.serve_captured:
+                    self.serve_kept.append(self.serve_ws)
+                elif self.serve_ws is not None:
+                    ws[:4] = self.serve_ws[:4]  # the status word
+                self.serve_ws, self.serve_captured = ws, False
+            self.serve_captured |= capturing
             yield self.serve_ws
         if cur != self.select_stream:
             cur.wait_stream(self.select_stream)
@@ -390,7 +398,7 @@ class PRRDecoder:
     def append_prompt(self, k_rows: torch.Tensor, v_rows: torch.Tensor, q_begin) -> None:
         """Append packed rows k_rows / v_rows [rows][Hkv][d] bf16 behind the sequences'
         tokens (sequence b: rows q_begin[b] .. q_begin[b+1]), with their block summaries."""
-        with self._serving(k_rows.shape[0]) as ws:
+        with self._serving() as ws:
             _abi.prr_append_prompt(self.dims, k_rows, v_rows, self._ints(q_begin), self.seq_lens, self.k_cache,
                                    self.v_cache, self.summ, ws)
 
@@ -422,10 +430,12 @@ class PRRDecoder:
         return out, lse
 
     def device_status(self) -> int:
-        """Device status code of the steps, or if that is 0 of the calls around them."""
-        code = _abi.prr_get_device_status(self.ws)
-        if code == 0 and self.serve_ws is not None:
-            code = _abi.prr_get_device_status(self.serve_ws)
+        """Device status code of the steps, or if that is 0 of the calls around them, captured
+        ones included (prr_workspace_init clears the one that reported: ws, serve_ws or one of serve_kept)."""
+        for ws in (self.ws, self.serve_ws, *self.serve_kept):
+            code = 0 if ws is None else _abi.prr_get_device_status(ws)
+            if code:
+                break
         return code
 
 

@@ -298,3 +298,44 @@ def test_a_token_without_a_page_is_dropped_and_can_be_given_again(mode, n, entry
     w = torch.softmax(torch.einsum("hd,nhd->hn", q[0].double(), kk) / 8, -1)
     # weights in two bf16 parts (2^-16 of each), fp32 sums
     assert (dec.out[0] - torch.einsum("hn,nhd->hd", w, vv)).abs().max() < 2.0 ** -13
+
+
+# ----------------------------------------------------------------------------- captured calls
+
+def test_a_captured_call_keeps_its_workspace_when_a_later_call_needs_a_larger_one():
+    Hq, Hkv, d, n, small = 8, 2, 64, 6000, 40
+    dec = prr.PRRDecoder(prr.Dims(B=1, Hq=Hq, Hkv=Hkv, d=d, bs=64, cap_tokens=n, K=4, P=0, pages=100), empty=True)
+    c = Case(Hq, Hkv, d, 64, [n], False)
+    k, v = (x[0].transpose(0, 1).contiguous() for x in (c.k, c.v))
+    q = c.randn(n, Hq, d)
+    dec.reserve([n])
+    dec.append_prompt(k[:small], v[:small], [0, small])
+    qb, qs = _i32([0, small]), q[:small].contiguous()
+    want, want_lse = dec.attend_prompt(qs, qb)
+    torch.cuda.synchronize()
+    used = dec.serve_ws.numel()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = dec.attend_prompt(qs, qb)
+    dec.append_prompt(k[small:], v[small:], [0, n - small])
+    assert dec.serve_ws.numel() == used  # appended rows take no room there
+    o, l = dec.attend_prompt(q, [0, n])
+    assert dec.serve_ws.numel() > used
+    c.check(q, o, l, _some((i, 0, i + 1) for i in range(n)))
+    with torch.cuda.stream(dec.select_stream):  # whatever was given back is in use again
+        junk = [torch.full((used,), 171, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    dec.seq_lens.fill_(small)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert all(bool((x == 171).all()) for x in junk)
+    assert dec.device_status() == 0
+    dec.seq_lens.fill_(small - 1)  # fewer tokens than rows: the replay's own status is read too
+    graph.replay()
+    torch.cuda.synchronize()
+    assert dec.device_status() == 1
