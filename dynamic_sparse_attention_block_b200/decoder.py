@@ -193,7 +193,8 @@ class PRRDecoder:
     # ------------------------------------------------------------------ setup
     def load_context(self, b: int, h: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """Write tokens [0, n) of sequence b, KV head h (k, v: [n][d] bf16 on the device)
-        into the cache, through the block table when the cache is paged."""
+        into the cache, through the block table when the cache is paged (whose blocks
+        must have their pages)."""
         n, bs = k.shape[0], self.dims.bs
         if self.block_table is None:
             self.k_cache[b, h, :n].copy_(k)
@@ -201,6 +202,8 @@ class PRRDecoder:
             return
         nbk = -(-n // bs)
         pages = self.block_table[b, :nbk].long()
+        if bool(((pages < 0) | (pages >= self.dims.pages)).any()):  # (-1 as an index would name the pool's last page)
+            raise ValueError(f"sequence {b} has no pages for {n} tokens: reserve() them first")
         pad = nbk * bs - n  # rows past n in the last page are never read
         kp = torch.nn.functional.pad(k, (0, 0, 0, pad)).view(nbk, bs, -1)
         vp = torch.nn.functional.pad(v, (0, 0, 0, pad)).view(nbk, bs, -1)

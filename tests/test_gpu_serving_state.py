@@ -339,3 +339,22 @@ def test_a_captured_call_keeps_its_workspace_when_a_later_call_needs_a_larger_on
     graph.replay()
     torch.cuda.synchronize()
     assert dec.device_status() == 1
+
+
+def test_load_context_needs_the_pages_it_writes():
+    dec = prr.PRRDecoder(prr.Dims(B=2, Hq=4, Hkv=1, d=64, bs=64, cap_tokens=512, K=4, P=0, pages=6), empty=True)
+    k, v = _tokens(130, 1, 1, d=64)
+    dec.reserve([0, 64])
+    for n in (1, 65, 130):
+        for b in (0, 1):
+            if (b, n) != (1, 1):
+                with pytest.raises(ValueError, match="reserve"):
+                    dec.load_context(b, 0, k[:n, 0], v[:n, 0])
+    assert not bool(dec.k_cache.any()) and not bool(dec.v_cache.any())
+    dec.reserve([130, 0])
+    dec.load_context(0, 0, k[:, 0], v[:, 0])
+    pages = dec.block_table[0, :3].long()
+    assert torch.equal(dec.k_cache[pages, 0].reshape(-1, 64)[:130], k[:, 0])
+    dec.block_table[0, 1] = 6  # past the pool
+    with pytest.raises(ValueError, match="reserve"):
+        dec.load_context(0, 0, k[:, 0], v[:, 0])
