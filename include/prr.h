@@ -515,8 +515,9 @@ prr_status prr_cache_reserve(const prr_dims* dims, const int32_t* want_lens,
  * order of i; pages that the parent holds beyond its length stay its own.  Summaries,
  * representative offsets and EMA entries of the parent's blocks and its prediction are
  * copied where the buffers are given; EMA entries behind them become 0.  A child that is
- * not empty, an index outside [0, B), and all but the first of several entries for one
- * child set PRR_DEV_BAD_RANGE and are skipped; too few free pages set PRR_DEV_NO_PAGES
+ * not empty, an index outside [0, B), a parent that the call also names as a child, and
+ * all but the first of several entries for one child set PRR_DEV_BAD_RANGE and are
+ * skipped; too few free pages set PRR_DEV_NO_PAGES
  * and change nothing.  n <= B.  Needs all buffers but the last four. */
 prr_status prr_cache_fork(const prr_dims* dims, const int32_t* parents, const int32_t* children,
                           int32_t n, const prr_cache_buffers* cache, void* ws, size_t ws_bytes,

@@ -358,3 +358,35 @@ def test_load_context_needs_the_pages_it_writes():
     dec.block_table[0, 1] = 6  # past the pool
     with pytest.raises(ValueError, match="reserve"):
         dec.load_context(0, 0, k[:, 0], v[:, 0])
+
+
+# ----------------------------------------------------------------------------- forks in one call
+
+@pytest.mark.parametrize("parents,children,done", [
+    ([0, 1], [2, 3], {2: 0, 3: 1}),
+    ([0, 1], [1, 2], {}),           # 1 is not empty, and as a child of the call no parent either
+    ([0, 2], [2, 3], {2: 0}),       # a chain: 2 becomes a copy of 0, 3 gets nothing
+    ([2, 0], [3, 2], {2: 0}),       # in the other order too
+    ([0, 0], [0, 2], {}),           # its own child
+    ([2, 0], [3, 4], {3: 2, 4: 0}),  # a copy of an empty sequence is empty
+])
+def test_fork_entries_that_name_each_other(parents, children, done):
+    lens = [100, 64, 0, 0, 0]
+    table, refs = _i32([[3, 1], [5, -1], [-1, -1], [-1, -1], [-1, -1]]), _i32([0, 1, 0, 1, 0, 1, 0, 0])
+    dims = prr.Dims(B=5, Hq=1, Hkv=1, d=64, bs=64, cap_tokens=128, K=1, P=0, pages=8, block_table=table.data_ptr())
+    kc = torch.arange(8, device=DEV).view(8, 1, 1, 1).expand(8, 1, 64, 64).bfloat16().contiguous()
+    vc, n = kc.clone(), _i32(lens)
+    ws = torch.zeros(prr.prr_serving_workspace_bytes(dims, 1), dtype=torch.uint8, device=DEV)
+    want, free, held = table.tolist(), iter([0, 2, 4]), refs.tolist()
+    for p, c in zip(parents, children):
+        if done.get(c) == p:
+            lens[c] = lens[p]
+            for j in range(lens[p] // 64):
+                want[c][j] = want[p][j]
+                held[want[p][j]] += 1
+            if lens[p] % 64:
+                want[c][lens[p] // 64] = pg = next(free)
+                held[pg] = 1
+    prr.prr_cache_fork(dims, _i32(parents), _i32(children), prr.cache_buffers(kc, vc, table, refs, n), ws)
+    assert prr.prr_get_device_status(ws) == (0 if len(done) == len(children) else 5)
+    assert table.tolist() == want and refs.tolist() == held and n.tolist() == lens
