@@ -34,7 +34,9 @@
 // of a measured matrix product; bound by the softmax's latency and the products (tensor pipe 75% busy; Q K^T with
 // 64 columns is limited by shared memory, 48 clocks where 128 columns take 64).  One step of 128 tokens
 // without S ahead: 900 TFLOP/s.  64 queries of 64/8 heads on four prefixes of 128K: 490 to 520 us,
-// 4.3 to 4.6 TB/s or 66 to 70% of a measured copy.
+// 4.3 to 4.6 TB/s or 66 to 70% of a measured copy; the prefixes alone in 370 to 420 us.  Pieces of 1024 rows of two
+// prompts behind 63K tokens (64/8 heads, caches of 0.53 GB): 920 to 1010 TFLOP/s, with 15.8 GB read from DRAM, as the CTAs
+// of a head stand at unrelated tokens; the same work on caches that stay in L2 (37 MB) 1240.
 #include "prr_serving.cuh"
 #include "prr_tensor.cuh"
 
@@ -872,8 +874,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
           }
         }
         // Each thread has one row; 64 bytes of the warp's rows at a time go through shared memory, so
-        // that four threads store 64 consecutive bytes of a row; few rows go straight out (a batch of 64 sequences
-        // with four prefixes of 128K: 513 us through shared memory, 503 us so).
+        // that four threads store 64 consecutive bytes of a row; few rows go straight out.  (No row straight out, up to
+        // 16, all: 64 sequences on four prefixes of 128K 471, 457, 451 us; 16 on one of 16K, one head a group, 51, 47,
+        // 47; 16 ragged prompts 88, 88, 96; one of 2048 rows 82, 82, 88; 256 of 64 tokens each on four prefixes of 1K
+        // 104, 104, 108.)
         char* own = row < 0 ? nullptr : direct ? reinterpret_cast<char*>(a.out + at * D) : reinterpret_cast<char*>(part + 4);
         char* to[4];
 #pragma unroll
@@ -952,7 +956,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 constexpr int kMergeWarps = 4;
 
 // Merge the n partial rows that row_of(i) names and write the result.  Few rows: one warp
-// (rows of different warps are different results).
+// (rows of different warps are different results).  With a CTA to every result: 16 ragged prompts 113 us, 88 so; a prompt
+// of 2048 rows 111 and 82; 64 sequences on four prefixes of 128K 471 and 457; where most tiles have many pieces (4 prompts of
+// 32 rows behind 16K) 80 and 82.
 template <int D, int kFewRows, typename RowOf>
 __device__ void merge_few(const Plan& plan, const AttendArgs& a, int n, size_t at, RowOf row_of) {
   constexpr int C = D / 32;

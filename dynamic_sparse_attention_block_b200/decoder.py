@@ -333,6 +333,7 @@ class PRRDecoder:
     # ------------------------------------------------------------------ around the step
     # Prompts and pages.  These run on the step stream, after the caller's current stream;
     # the caller's stream then waits for them, so their results can be used on it at once.
+    # They share one workspace: replays of captured ones, too, run one after another.
 
     @contextlib.contextmanager
     def _serving(self, rows: int = 1):
@@ -364,7 +365,8 @@ class PRRDecoder:
         return torch.as_tensor(x, dtype=torch.int32).to(self.device).contiguous()
 
     def cache_buffers(self) -> _abi.PrrCacheBuffers:
-        """The paged cache and the state that goes with its sequences (prr_cache_* calls)."""
+        """The paged cache and the state that goes with its sequences (prr_cache_* calls),
+        with the prediction that is current now: a step makes it the other one."""
         if self.page_refs is None:
             raise ValueError("pages are shared, reserved and moved in a paged cache only (dims.pages > 0)")
         return _abi.cache_buffers(self.k_cache, self.v_cache, self.block_table, self.page_refs, self.seq_lens, self.summ,

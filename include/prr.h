@@ -445,7 +445,9 @@ size_t prr_serving_workspace_bytes(const prr_dims* dims, int32_t max_rows);
  * are extended (summ NULL: left alone), as prr_update_summaries does; then seq_lens[b]
  * grows by the sequence's rows.  A sequence that would pass cap_tokens, or whose length
  * is negative, sets PRR_DEV_BAD_SEQ_LEN and stays as it was.  A row whose block has no
- * page (a table entry outside [0, pages)) is dropped and sets PRR_DEV_BAD_RANGE. */
+ * page (a table entry outside [0, pages)) is dropped and sets PRR_DEV_BAD_RANGE; its
+ * sequence's length counts it all the same, so release the sequence before it is used
+ * again. */
 prr_status prr_append_prompt(const prr_dims* dims, const uint16_t* k_rows, const uint16_t* v_rows,
                              int64_t row_stride, const int32_t* q_begin, int32_t rows,
                              int32_t* seq_lens, uint16_t* k_cache, uint16_t* v_cache,
@@ -454,8 +456,8 @@ prr_status prr_append_prompt(const prr_dims* dims, const uint16_t* k_rows, const
 /* Causal attention of packed prompt rows q [rows][Hq][d] bf16 over the caches, which
  * hold the rows' own tokens already (prr_append_prompt): the l rows of sequence b are
  * its newest l of seq_lens[b] tokens, and row i attends the tokens at positions
- * 0 .. seq_lens[b]-l+i.  out [rows][Hq][d] bf16, lse [rows][Hq] fp32 (NULL: not
- * written); only the sequences' rows are written.  A sequence with more rows than
+ * 0 .. seq_lens[b]-l+i.  out [rows][Hq][d] bf16 (not overlapping q), lse [rows][Hq] fp32
+ * (NULL: not written); only the sequences' rows are written.  A sequence with more rows than
  * tokens, or a length outside [1, cap_tokens], sets PRR_DEV_BAD_SEQ_LEN and is skipped.
  * Cache rows at or past seq_lens[b] may hold anything (NaN included); those below it are
  * finite.  A row and head of q that is not finite, or whose products with the keys all
@@ -473,7 +475,7 @@ prr_status prr_attend_prompt(const prr_dims* dims, const uint16_t* q, int64_t q_
  * the cache (its part of the block table), and must be full: shared_blocks[g]*bs <=
  * seq_lens of every member.  0 shares nothing.  out [B][Hq][d] bf16, lse [B][Hq] fp32
  * (NULL: not written), written for the members only; a member of length 0 gets zeros and
- * -infinity.  A member outside [0, B), a group whose range or shared_blocks is out of
+ * -infinity, and a query that is not finite what prr_attend_prompt gives it.  A member outside [0, B), a group whose range or shared_blocks is out of
  * range for it (PRR_DEV_BAD_RANGE), or a length outside [0, cap_tokens]
  * (PRR_DEV_BAD_SEQ_LEN) is skipped.  Two entries for one sequence both compute its row. */
 prr_status prr_attend_shared(const prr_dims* dims, const uint16_t* q, int64_t q_stride,
