@@ -47,7 +47,6 @@ namespace {
 constexpr int kBlock = 128;         // tokens per unit of work
 constexpr int kStep = 64;           // tokens per product: two steps of S in tensor memory, one ahead
 constexpr float kGrow = 8.0f;       // log2 of the growth that moves the reference m
-constexpr int kPlanThreads = 1024;
 constexpr int kAttendThreads = 384;  // 2 x 128 softmax threads; two warps for products, one for copies, one for Q
 
 __host__ __device__ constexpr int sub_tokens(int G) { return kBlock / G; }  // packed tokens per 128 rows
@@ -94,33 +93,6 @@ __device__ __forceinline__ int cta_of(long long units, int ctas, long long z) {
 }
 
 // ------------------------------------------------------------------ the plan
-
-template <typename T>
-__device__ T plan_scan(T v, T* total) {  // exclusive prefix sum over the CTA
-  __shared__ T warp_sum[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  T x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sum[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    T s = warp_sum[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sum[lane] = s;
-  }
-  __syncthreads();
-  *total = warp_sum[kPlanThreads / 32 - 1];
-  return x - v + (w ? warp_sum[w - 1] : 0);
-}
 
 // The plan's small inputs and its prefix sums are searched in shared memory where they fit.
 constexpr int kPlanSeqs = 2048, kPlanSlots = 2048;
@@ -260,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       plan.tile[slot] = t;
     }
     long long total;
-    const long long at = sum + plan_scan<long long>(t.blocks, &total);
+    const long long at = sum + cta_scan<long long>(t.blocks, &total);
     if (slot < slots) plan.prefix[slot] = prefix[slot] = at;
     sum += total;
   }

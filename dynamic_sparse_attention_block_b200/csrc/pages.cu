@@ -13,7 +13,6 @@ namespace prr {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanEach = 8;  // neighbouring pages a thread looks at between two scans
 
 // Page bookkeeping in the workspace, int32 words.
@@ -41,33 +40,6 @@ __host__ __device__ inline PageWork page_work(int* w, int B, int pages) {
   return x;
 }
 
-// Exclusive prefix sum of v over the CTA's kPlanThreads threads; *total = the sum.
-__device__ int cta_scan(int v, int* total) {
-  __shared__ int warp_sum[kPlanThreads / 32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // the previous scan's readers are done
-  if (lane == 31) warp_sum[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    int s = warp_sum[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sum[lane] = s;
-  }
-  __syncthreads();
-  *total = warp_sum[kPlanThreads / 32 - 1];
-  return x - v + (w ? warp_sum[w - 1] : 0);
-}
-
 // The `need` lowest free pages, ascending, into list.  Returns how many there are (need,
 // or fewer).
 __device__ int find_free(const int* refs, int pages, int need, int* list) {
@@ -87,14 +59,15 @@ __device__ int find_free(const int* refs, int pages, int need, int* list) {
   return found;
 }
 
-// Exclusive prefix sums over need[0..n) in place; returns the sum.
-__device__ int scan_needs(int* need, int n) {
-  int sum = 0;
+// Exclusive prefix sums over need[0..n) in place; returns the sum, which may pass 32 bits (a table can have more
+// entries; the sums in place then mean nothing).
+__device__ long long scan_needs(int* need, int n) {
+  long long sum = 0;
   for (int base = 0; base < n; base += kPlanThreads) {
     const int i = base + threadIdx.x;
-    int total;
-    const int at = sum + cta_scan(i < n ? need[i] : 0, &total);
-    if (i < n) need[i] = at;
+    long long total;
+    const long long at = sum + cta_scan<long long>(i < n ? need[i] : 0, &total);
+    if (i < n) need[i] = static_cast<int>(at);
     sum += total;
   }
   __syncthreads();
@@ -126,9 +99,9 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
     if (lane == 0) w.need[b] = n;
   }
   __syncthreads();
-  const int need = scan_needs(w.need, p.B);
+  const long long need = scan_needs(w.need, p.B);
   if (need == 0) return;
-  if (find_free(a.refs, p.pages, need, w.list) < need) {
+  if (need > p.pages || find_free(a.refs, p.pages, static_cast<int>(need), w.list) < need) {
     if (threadIdx.x == 0) report(p.status, kDevNoPages);
     return;
   }
@@ -185,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_co
     w.need[i] = src >= 0;
   }
   __syncthreads();
-  const int need = scan_needs(w.need, n);
+  const int need = static_cast<int>(scan_needs(w.need, n));  // at most n
   const bool enough = need == 0 || find_free(a.refs, p.pages, need, w.list) == need;
   if (!enough && threadIdx.x == 0) report(p.status, kDevNoPages);
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {

@@ -25,6 +25,36 @@ __device__ __forceinline__ bool packed_range(const int* q_begin, int b, int rows
   return false;
 }
 
+constexpr int kPlanThreads = 1024;  // of the one CTA that plans a call
+
+// Exclusive prefix sum of v over a CTA of kPlanThreads threads; *total = the sum.
+template <typename T>
+__device__ T cta_scan(T v, T* total) {
+  __shared__ T warp_sum[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the previous scan's readers are done
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    T s = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sum[lane] = s;
+  }
+  __syncthreads();
+  *total = warp_sum[kPlanThreads / 32 - 1];
+  return x - v + (w ? warp_sum[w - 1] : 0);
+}
+
 struct AppendArgs {
   const uint16_t* k_rows;
   const uint16_t* v_rows;

@@ -390,3 +390,21 @@ def test_fork_entries_that_name_each_other(parents, children, done):
     prr.prr_cache_fork(dims, _i32(parents), _i32(children), prr.cache_buffers(kc, vc, table, refs, n), ws)
     assert prr.prr_get_device_status(ws) == (0 if len(done) == len(children) else 5)
     assert table.tolist() == want and refs.tolist() == held and n.tolist() == lens
+
+
+# ----------------------------------------------------------------------------- reservations past 32 bits
+
+def test_a_reservation_of_more_blocks_than_32_bits_count_changes_nothing():
+    B, bs, cap = 128, 64, 1 << 30  # 2^31 blocks are asked for: as 32 bits, a negative number
+    table = torch.full((B, cap // bs), -1, dtype=torch.int32, device=DEV)
+    refs, lens = _i32([0, 1, 0, 0]), _i32([0] * B)
+    dims = prr.Dims(B=B, Hq=1, Hkv=1, d=64, bs=bs, cap_tokens=cap, K=1, P=0, pages=4, block_table=table.data_ptr())
+    ws = torch.zeros(prr.prr_serving_workspace_bytes(dims, 1), dtype=torch.uint8, device=DEV)
+    bufs = prr.cache_buffers(block_table=table, page_refs=refs, seq_lens=lens)
+    prr.prr_cache_reserve(dims, _i32([cap] * B), bufs, ws)
+    assert prr.prr_get_device_status(ws) == 6
+    assert refs.tolist() == [0, 1, 0, 0] and int(table.max()) == -1
+    prr.prr_workspace_init(ws)
+    prr.prr_cache_reserve(dims, _i32([bs] * 3 + [0] * (B - 3)), bufs, ws)
+    assert prr.prr_get_device_status(ws) == 0
+    assert refs.tolist() == [1] * 4 and table[:4, :2].tolist() == [[0, -1], [2, -1], [3, -1], [-1, -1]]
